@@ -17,10 +17,13 @@ STATUS_NAMES = {0: "DLLM_OK", 1: "DLLM_ERR_ARG", 2: "DLLM_ERR_SHAPE", 3: "DLLM_E
 DLLM_FP32, DLLM_BF16 = 0, 1
 MAX_L, MAX_ROWS, MAX_POSITIONS, MAX_QUEUE = 1024, 4096, 262144, 8192
 NOALLOC_SCRATCH_BYTES = 16 << 20
+MAX_TOP, MAX_TOKENS, MAX_VOCAB, MAX_WIDTH = 32, 1 << 24, 1 << 24, 1 << 20
 
 EXPORTS = ("dllm_step", "dllm_step_noalloc", "dllm_step_timed", "dllm_step_score", "dllm_step_score_timed", "dllm_step_decide", "dllm_step_quota", "dllm_step_decide_quota",
            "dllm_step_features", "dllm_step_score_shard", "dllm_step_decide_shards", "dllm_shard_triples_bytes",
-           "dllm_step_workspace_bytes", "dllm_pack", "dllm_compact", "dllm_last_error")
+           "dllm_step_workspace_bytes", "dllm_pack", "dllm_compact", "dllm_logprobs", "dllm_logprobs_grad",
+           "dllm_logprobs_workspace_bytes", "dllm_embed", "dllm_embed_grad", "dllm_embed_grad_workspace_bytes",
+           "dllm_last_error")
 
 
 class DllmError(RuntimeError):
@@ -59,6 +62,7 @@ def lib():
                                "(or __graft_entry__.build()); there is no fallback path")
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        f32 = ctypes.c_float
         L.dllm_step.argtypes = [vp, vp, i32, i64, i64, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp,
                                 vp, vp, vp, sz, vp]
         L.dllm_step.restype = i32
@@ -98,6 +102,20 @@ def lib():
         L.dllm_compact.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, ctypes.POINTER(Reqs),
                                    ctypes.POINTER(Queue), i64, vp, vp]
         L.dllm_compact.restype = i32
+        L.dllm_logprobs_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.dllm_logprobs_workspace_bytes.restype = sz
+        L.dllm_logprobs.argtypes = [vp, vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, i64, i32, vp, vp, vp, vp, vp,
+                                    vp, sz, vp]
+        L.dllm_logprobs.restype = i32
+        L.dllm_logprobs_grad.argtypes = [vp, vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, i64, vp, vp, vp, vp, vp,
+                                         i64, i64, vp]
+        L.dllm_logprobs_grad.restype = i32
+        L.dllm_embed.argtypes = [vp, vp, i32, i64, i32, i32, vp, vp, i32, f32, vp, i32, i64, vp]
+        L.dllm_embed.restype = i32
+        L.dllm_embed_grad_workspace_bytes.argtypes = [i32, i32, i32]
+        L.dllm_embed_grad_workspace_bytes.restype = sz
+        L.dllm_embed_grad.argtypes = [vp, vp, i32, i64, vp, vp, i32, f32, i32, i32, vp, i32, i64, i32, vp, sz, vp]
+        L.dllm_embed_grad.restype = i32
         # the HIP runtime's event calls, reached through this library's own dependency (the same
         # runtime torch uses), for the kernel-bound timing of dllm_step_score_timed
         L.hipEventCreate.argtypes = [ctypes.POINTER(vp)]

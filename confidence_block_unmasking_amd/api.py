@@ -312,6 +312,182 @@ def dllm_step_features(rows, L, row_req, reqs: "ReqTable", conf, mask_out, featu
     _lib.check(rc, "dllm_step_features")
 
 
+# ---- log probabilities and embeddings: the two sides of the forward ------------------------------
+
+def _call(fn, where, stream, tensors, *args):
+    """fn(stream, *args) on the device that all `tensors` share (None entries aside), whatever the
+    current device is; `stream`, when given, must be that device's."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{where}: tensors on {dev} and {t.device}; all must be on one device")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{where}: stream of {stream.device} for tensors on {dev}")
+    if dev.index == torch.cuda.current_device():
+        rc = fn(_stream(stream), *args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(_stream(stream), *args)
+    _lib.check(rc, where)
+
+
+def _tokens_arg(tokens, rows, L):
+    """Row stride of int32 tokens [rows, L]: a contiguous tensor, or a 2-D view with unit column
+    stride (such as box[:, W - L:])."""
+    if not tokens.is_cuda or tokens.dtype != torch.int32:
+        raise ValueError(f"tokens must be an int32 device tensor, got {tokens.dtype} on {tokens.device}")
+    if tokens.dim() == 2:
+        if tokens.shape[0] < rows or tokens.shape[1] < L:
+            raise ValueError(f"tokens of shape {tuple(tokens.shape)}, needs [{rows}, {L}]")
+        if L > 1 and tokens.stride(1) != 1:
+            raise ValueError("tokens must have unit stride along a row")
+        return tokens.stride(0) if tokens.shape[0] > 1 else max(tokens.stride(0), L)
+    _need(tokens, torch.int32, "tokens", rows * L)
+    return L
+
+
+def dllm_logprobs_workspace_bytes(rows: int, L: int, V: int, k: int = 0, dtype=torch.bfloat16) -> int:
+    return int(_lib.lib().dllm_logprobs_workspace_bytes(rows, L, V, k, _DT[dtype]))
+
+
+def new_logprobs_workspace(rows: int, L: int, V: int, k: int = 0, dtype=torch.bfloat16, device="cuda"):
+    """A dllm_logprobs workspace for this shape (no particular contents are needed)."""
+    return torch.empty(max(dllm_logprobs_workspace_bytes(rows, L, V, k, dtype), 256), dtype=torch.uint8, device=device)
+
+
+def dllm_logprobs(logits, mask, tokens, logprob, workspace, status, entropy=None, stats=None, top_ids=None,
+                  top_logprobs=None, k=None, exclude=None, rows=None, L=None, V=None, pos_stride=None, row_stride=None,
+                  stream=None):
+    """Log probabilities of `tokens` at the selected slots (mask nonzero, exclude zero), with entropy,
+    softmax statistics and the top k alternatives where those outputs are given (see include/dllm.h).
+
+    logits as for dllm_step, at any alignment; tokens int32 [rows, L] (a view of the box's block
+    columns will do) or None with logprob None; logprob, entropy float32 [rows, L]; stats float32
+    [rows, L, 2]; top_ids int32 and top_logprobs float32 [rows, L, k] (k: top_ids' last dimension
+    unless given).  Slots that are not selected keep what the outputs held."""
+    rows, L, V, pos_stride, row_stride = _logits_shape(logits, rows, L, V, pos_stride, row_stride)
+    _need(mask, torch.uint8, "mask", rows * L)
+    _need(workspace, torch.uint8, "workspace")
+    _need(status, torch.int32, "status", 1)
+    if exclude is not None:
+        _need(exclude, torch.uint8, "exclude", rows * L)
+    token_stride = L
+    if tokens is not None:
+        token_stride = _tokens_arg(tokens, rows, L)
+    if k is None:
+        k = top_ids.shape[-1] if top_ids is not None else 0
+    for t, dt, nm, n in ((logprob, torch.float32, "logprob", rows * L), (entropy, torch.float32, "entropy", rows * L),
+                         (stats, torch.float32, "stats", rows * L * 2), (top_ids, torch.int32, "top_ids", rows * L * k),
+                         (top_logprobs, torch.float32, "top_logprobs", rows * L * k)):
+        if t is not None:
+            _need(t, dt, nm, n)
+    _call(_lib.lib().dllm_logprobs, "dllm_logprobs", stream,
+          (logits, mask, exclude, tokens, logprob, entropy, stats, top_ids, top_logprobs, workspace, status),
+          _ptr(logits), _DT[logits.dtype], pos_stride, row_stride, rows, L, V, _ptr(mask), _ptr(exclude), _ptr(tokens),
+          token_stride, int(k), _ptr(logprob), _ptr(entropy), _ptr(stats), _ptr(top_ids), _ptr(top_logprobs),
+          _ptr(workspace), workspace.numel(), _ptr(status))
+
+
+def dllm_logprobs_grad(logits, mask, tokens, stats, grad_logprob, grad_logits, status, entropy=None, grad_entropy=None,
+                       exclude=None, rows=None, L=None, V=None, pos_stride=None, row_stride=None, grad_pos_stride=None,
+                       grad_row_stride=None, stream=None):
+    """Gradient of dllm_logprobs' log probabilities (grad_logprob) and entropies (grad_entropy) with
+    respect to the logits, into every slot of grad_logits (the logits' dtype; zeros where not
+    selected).  stats and entropy are the forward's outputs.  grad_logits may be logits itself."""
+    rows, L, V, pos_stride, row_stride = _logits_shape(logits, rows, L, V, pos_stride, row_stride)
+    if grad_logits.dtype != logits.dtype:
+        raise ValueError(f"grad_logits must be {logits.dtype}, got {grad_logits.dtype}")
+    if grad_logits.dim() == 3 and tuple(grad_logits.shape) != (rows, L, V):
+        raise ValueError(f"grad_logits of shape {tuple(grad_logits.shape)}, needs [{rows}, {L}, {V}]")
+    _, _, _, grad_pos_stride, grad_row_stride = _logits_shape(grad_logits, rows, L, V, grad_pos_stride, grad_row_stride)
+    _need(mask, torch.uint8, "mask", rows * L)
+    _need(stats, torch.float32, "stats", rows * L * 2)
+    _need(status, torch.int32, "status", 1)
+    token_stride = L
+    if tokens is not None:
+        token_stride = _tokens_arg(tokens, rows, L)
+    for t, dt, nm in ((exclude, torch.uint8, "exclude"), (grad_logprob, torch.float32, "grad_logprob"),
+                      (entropy, torch.float32, "entropy"), (grad_entropy, torch.float32, "grad_entropy")):
+        if t is not None:
+            _need(t, dt, nm, rows * L)
+    _call(_lib.lib().dllm_logprobs_grad, "dllm_logprobs_grad", stream,
+          (logits, mask, exclude, tokens, stats, grad_logprob, entropy, grad_entropy, grad_logits, status),
+          _ptr(logits), _DT[logits.dtype], pos_stride, row_stride, rows, L, V, _ptr(mask), _ptr(exclude), _ptr(tokens),
+          token_stride, _ptr(stats), _ptr(grad_logprob), _ptr(entropy), _ptr(grad_entropy), _ptr(grad_logits),
+          grad_pos_stride, grad_row_stride, _ptr(status))
+
+
+def _matrix(t, name):
+    """(rows, columns, row stride) of a device matrix: a 2-D tensor with unit column stride, or a
+    contiguous tensor of any shape taken as [-1, its last dimension]."""
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype not in _DT:
+        raise ValueError(f"{name} dtype {t.dtype} not supported")
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    D = t.shape[-1]
+    if t.dim() == 2:
+        if D > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit stride along a row")
+        return t.shape[0], D, t.stride(0) if t.shape[0] > 1 else max(t.stride(0), D)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or 2-D")
+    return (t.numel() // D if D else 0), D, D
+
+
+def _ids_arg(ids, valid, status):
+    _need(ids, torch.int32, "ids")
+    if valid is not None:
+        _need(valid, torch.uint8, "valid", ids.numel())
+    _need(status, torch.int32, "status", 1)
+    return ids.numel()
+
+
+def dllm_embed(table, ids, out, status, valid=None, scale=1.0, stream=None):
+    """out[n] = scale * table[ids[n]], zeros where valid[n] == 0 (see include/dllm.h).  table
+    [n_vocab, D]; ids int32 and valid uint8 of any shape (a box's box_ids and box_valid); out
+    [ids.numel(), D] or ids' shape with D appended; fp32 or bf16 each.  Rows of out past the last
+    token keep what they held."""
+    n = _ids_arg(ids, valid, status)
+    n_vocab, D, ts = _matrix(table, "table")
+    n_out, D_out, os_ = _matrix(out, "out")
+    if D_out != D or n_out < n:
+        raise ValueError(f"out holds {n_out} rows of {D_out}, needs {n} of {D}")
+    _call(_lib.lib().dllm_embed, "dllm_embed", stream, (table, ids, valid, out, status),
+          _ptr(table), _DT[table.dtype], ts, n_vocab, D, _ptr(ids), _ptr(valid), n, float(scale), _ptr(out),
+          _DT[out.dtype], os_, _ptr(status))
+
+
+def dllm_embed_grad_workspace_bytes(n_tokens: int, n_vocab: int, D: int) -> int:
+    return int(_lib.lib().dllm_embed_grad_workspace_bytes(n_tokens, n_vocab, D))
+
+
+def new_embed_grad_workspace(n_tokens: int, n_vocab: int, D: int, device="cuda"):
+    """A dllm_embed_grad workspace for up to n_tokens tokens (no particular contents are needed)."""
+    return torch.empty(max(dllm_embed_grad_workspace_bytes(n_tokens, n_vocab, D), 256), dtype=torch.uint8, device=device)
+
+
+def dllm_embed_grad(grad_out, ids, grad_table, workspace, status, valid=None, scale=1.0, accumulate=False, stream=None):
+    """The gradient of dllm_embed with respect to its table: grad_table[v] = scale * the sum of
+    grad_out over the tokens of v, every row written; with accumulate, added to the rows that occur
+    (see include/dllm.h)."""
+    n = _ids_arg(ids, valid, status)
+    n_vocab, D, ts = _matrix(grad_table, "grad_table")
+    n_grad, D_grad, gs = _matrix(grad_out, "grad_out")
+    if D_grad != D or n_grad < n:
+        raise ValueError(f"grad_out holds {n_grad} rows of {D_grad}, needs {n} of {D}")
+    _need(workspace, torch.uint8, "workspace")
+    _call(_lib.lib().dllm_embed_grad, "dllm_embed_grad", stream,
+          (grad_out, ids, valid, grad_table, workspace, status),
+          _ptr(grad_out), _DT[grad_out.dtype], gs, _ptr(ids), _ptr(valid), n, float(scale), n_vocab, D,
+          _ptr(grad_table), _DT[grad_table.dtype], ts, int(bool(accumulate)), _ptr(workspace), workspace.numel(),
+          _ptr(status))
+
+
 class ReqTable:
     """Device-resident request table (the fields of dllm_reqs), built from host numpy arrays."""
 

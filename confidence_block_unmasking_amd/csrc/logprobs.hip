@@ -1,0 +1,710 @@
+// dllm_logprobs: log probabilities of given tokens at selected slots, with the distribution's entropy
+// and its top alternatives; dllm_logprobs_grad: their gradient with respect to the logits.
+//
+// What is computed ([DiLaServe] = page "DiLaServe: High SLO Attainment Serving for Diffusion Language
+// Models" §三 3.1: the softmax distribution over a masked slot's vocabulary logits, of which the step
+// keeps the largest probability only).  With x the V logits of a slot, m = max x and
+// S = sum exp(x - m):
+//   log p_v = x_v - m - log S;   entropy = log S - (1/S) sum exp(x - m) (x - m);
+//   alternatives = the k largest x, the lowest column first among equals.
+//
+// How (gfx950).  A streaming reduction over the selected slots' rows, bound by HBM, on the scoring
+// kernel's work split: rows are cut into chunks of 64*kVPL 16-byte vectors, a workgroup has an even
+// share of all selected slots' chunks, and its waves take chunks one at a time from an LDS counter.
+//   - One pass gives max, sum and the entropy's weighted sum T = sum e * y in base 2, with
+//     y = (x - m) log2 e and e = 2^y: the entropy costs a max and an FMA per element beside the
+//     unpack, max3, FMA, v_exp and add of the sum.  All terms of T have one sign, so the entropy
+//     has no cancellation.
+//   - y is one FMA, x*log2e - m*log2e.  The product m*log2e is rounded once per chunk; its residual r
+//     (exact, by an FMA) is taken out of the sums by a factor 2^-r, so large offsets of the logits
+//     cost no accuracy.  Chunks whose maximum lies beyond kNearMax subtract first instead.
+//   - Alternatives: each wave keeps the k best of the chunks it took from a slot sorted across its
+//     lanes (lane i holds the i-th best).  An element enters only if it beats the k-th; an insertion
+//     is a ballot, a count and one lane shift.  A wave's list starts from the k-th largest lane
+//     maximum of its first chunk (a lower bound of the k-th best, found by 16 ballots), and waves of a
+//     workgroup share the best k-th value seen per slot in LDS, so after the first chunks almost every
+//     chunk is passed over by one comparison per lane.  Elements are visited in column order and
+//     must be strictly better, which keeps the lowest column among equals; a row of equal logits
+//     costs k insertions per chunk at most.
+//   - A second kernel, one wave per slot, joins the chunk records in a fixed order, so the sums' bits
+//     do not depend on timing, merges the candidate lists under the full order (value, then column),
+//     and looks up the given token's logit.
+#include "elem_common.h"
+
+namespace {
+
+using namespace dllm;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFarBelow = -300.0f;           // base-2 exponent whose power is 0 in fp32 (2^-149 is the least)
+constexpr float kNearMax = 65536.0f;           // |m| up to which rounding m * log2e moves y by less than 2^-8
+constexpr int kNoKey = (int)0x80000000;        // below the key of every number
+
+struct LogprobParams {
+    const char *logits;
+    int64_t pos_stride_b, row_stride_b;        // strides in bytes
+    int32_t rows, L, V, NV, NC, k;
+    const uint8_t *mask, *exclude;             // selected: mask != 0 and (exclude NULL or exclude == 0)
+    const int32_t *tokens;
+    int64_t token_stride;
+    float *logprob, *entropy;
+    float2 *stats;
+    int32_t *top_ids;
+    float *top_lp;
+    float4 *partials;                          // [rows*L*NC] {max, sum, weighted sum, candidates listed}
+    int2 *cand;                                // [rows*L*NC*k] {key, column}
+    int32_t *status;
+};
+
+// Integer order of floats: larger value, larger key; -0 and +0 share one.
+__device__ __forceinline__ int order_key(float x) {
+    const int b = __float_as_int(x + 0.0f);
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float key_value(int key) { return __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF)); }
+
+// Selected slots among the 16 that start at s0, as bits.
+__device__ __forceinline__ uint32_t selected16(const LogprobParams &P, int s0, int S) {
+    uint32_t b = mask_bits16(P.mask, s0, S);
+    if (P.exclude != nullptr) b &= ~mask_bits16(P.exclude, s0, S);
+    return b;
+}
+
+// The kVPL loads of a chunk for this lane: its first nf vectors are whole; addresses past them are
+// clamped and their values replaced in widen().
+template <bool BF16>
+__device__ __forceinline__ void issue_chunk(u32x4 (&raw)[kVPL], const char *row, int vb, int nf) {
+    typedef typename Row<BF16>::vec vec;
+    const int lane = lane_id();
+    const vec *base = (const vec *)row + vb;
+    if (nf == kCH) {
+#pragma unroll
+        for (int k = 0; k < kVPL; ++k) raw[k] = __builtin_nontemporal_load(base + k * 64 + lane);
+    } else if (nf > 0) {
+#pragma unroll
+        for (int k = 0; k < kVPL; ++k) raw[k] = __builtin_nontemporal_load(base + min(k * 64 + lane, nf - 1));
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ void widen(const u32x4 (&raw)[kVPL], float (&x)[kVPL][Fmt<BF16>::E], const char *row, int vb,
+                                      int n, int nf, int V) {
+#pragma unroll
+    for (int k = 0; k < kVPL; ++k) unpack<BF16>(raw[k], x[k]);
+    if (nf < kCH) {
+        const int lane = lane_id();
+#pragma unroll
+        for (int k = 0; k < kVPL; ++k) {
+            const int v = k * 64 + lane;
+            if (v >= nf) {
+                if (v < n) {                   // the row's ragged last vector
+                    load_vec_elems<BF16>(row, vb + v, V, x[k]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < Fmt<BF16>::E; ++e) x[k][e] = -INFINITY;
+                }
+            }
+        }
+    }
+}
+
+// ---- the k best, one per lane in order ----------------------------------------------------------
+struct Best {
+    int key, col;                              // this lane's entry
+    int cut;                                   // key of entry k-1: what an element has to beat
+};
+__device__ __forceinline__ int up_one(int v) { return wave_dpp::mov<0x138>(v, v); }   // lane i reads lane i-1
+
+// Insert after `at` entries: the entries from there move up a lane.
+__device__ __forceinline__ void insert_at(Best &b, int at, int key, int col, int k) {
+    const int lane = lane_id();
+    const int mk = up_one(b.key), mc = up_one(b.col);
+    b.key = lane < at ? b.key : lane == at ? key : mk;
+    b.col = lane < at ? b.col : lane == at ? col : mc;
+    b.cut = __builtin_amdgcn_readlane(b.key, k - 1);
+}
+
+// A lower bound of the k-th largest of the 64 lanes' keys (exact in its upper 16 bits), minus one: the
+// floor that elements have to exceed.
+__device__ __forceinline__ int kth_floor(int key, int k) {
+    const uint32_t u = (uint32_t)key ^ 0x80000000u;
+    uint32_t t = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t trial = t | (1u << bit);
+        if (__popcll(__ballot(u >= trial)) >= k) t = trial;
+    }
+    return t == 0 ? kNoKey : (int)(t ^ 0x80000000u) - 1;
+}
+
+// Offer the vectors x[kk] of a chunk (column of lane l, element e: (vb + kk*64 + l)*E + e) whose
+// maximum exceeds the floor, in column order.
+template <int E>
+__device__ __forceinline__ void offer(Best &b, int floor, float (&x)[kVPL][E], float (&vm)[kVPL], int vb, int V, int k) {
+    const int lane = lane_id();
+#pragma unroll
+    for (int kk = 0; kk < kVPL; ++kk) {
+        const int vk = order_key(vm[kk]);
+        uint64_t hit = __ballot(vk > floor);
+        while (hit != 0) {
+            const int l = __builtin_ctzll(hit);
+            hit &= hit - 1;
+            // that vector's elements to lanes 0 .. E-1
+            int c = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                c = lane == e ? __builtin_amdgcn_readlane(__float_as_int(x[kk][e]), l) : c;
+            const int ck = order_key(__int_as_float(c));
+            const int col0 = (vb + kk * 64 + l) * E;
+            uint64_t in = __ballot(lane < E && col0 + lane < V && ck > floor);
+            while (in != 0) {
+                const int e = __builtin_ctzll(in);
+                const int key = __builtin_amdgcn_readlane(ck, e);
+                insert_at(b, __popcll(__ballot(b.key >= key)), key, col0 + e, k);
+                floor = max(floor, b.cut);
+                in &= in - 1;
+                in &= __ballot(ck > floor);
+            }
+            hit &= __ballot(vk > floor);
+        }
+    }
+}
+
+// Kernel 1: one record per chunk of every selected slot, and the candidate lists.
+template <bool BF16, bool ENT, bool TOP>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void logprob_chunks_kernel(LogprobParams P,
+                                                                                                          int win) {
+    extern __shared__ int s_id[];              // [win] selected slots of this workgroup's window; with TOP
+    int *s_cut = s_id + win;                   // [win] the best k-th key any wave holds for them
+    __shared__ int s_tmp[2][kWaves];
+    __shared__ int s_next;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = uni(tid >> 6);
+    const int L = P.L, S = P.rows * L, NC = P.NC;
+    const int ntiles = (S + kTile - 1) / kTile;
+
+    // 0. Number the selected slots in slot order (16 per thread and tile), split their chunks evenly
+    //    over the workgroups and list this workgroup's slots in LDS.
+    const uint32_t mb0 = selected16(P, tid * 16, S);
+    fetch_args(P.logits, P.row_stride_b, P.pos_stride_b, P.partials, P.NV, P.V, P.k);
+    int more_cnt = 0;
+    for (int t = 1; t < ntiles; ++t) more_cnt += __popc(selected16(P, t * kTile + tid * 16, S));
+    // slots selected before this thread's 16 in its tile, and in the whole tile
+    auto place = [&](uint32_t mb, int *tmp, int &before, int &total) {
+        const int c = __popc(mb);
+        const int incl = wave_incl_scan(c);
+        if (lane == 63) tmp[wave] = incl;
+        __syncthreads();
+        before = incl - c;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const int v = tmp[w];
+            before += w < wave ? v : 0;
+            total += v;
+        }
+    };
+    int before, base;
+    place(mb0, s_tmp[0], before, base);
+    int M = base;
+    if (ntiles > 1) M += block_sum(more_cnt, s_tmp[1]);
+    M = uni(M);
+    const int I = M * NC;                      // chunk t is chunk t % NC of selected slot t / NC
+    const int G = gridDim.x, g = blockIdx.x;
+    const int per = I / G, rem = I - per * G;
+    const int t0 = g * per + min(g, rem), t1 = t0 + per + (g < rem ? 1 : 0);
+    if (t0 >= t1) return;                      // uniform over the workgroup
+    const int q_lo = t0 / NC, q_hi = (t1 - 1) / NC;
+    auto list = [&](uint32_t mb, int q, int s0) {
+        for (; mb != 0 && q <= q_hi; ++q) {
+            if (q >= q_lo) s_id[q - q_lo] = s0 + __builtin_ctz(mb);
+            mb &= mb - 1;
+        }
+    };
+    list(mb0, before, tid * 16);
+    for (int t = 1; t < ntiles && base <= q_hi; ++t) {
+        const uint32_t mb = selected16(P, t * kTile + tid * 16, S);
+        int total;
+        __syncthreads();                       // the previous user of s_tmp[1] is done
+        place(mb, s_tmp[1], before, total);
+        list(mb, base + before, t * kTile + tid * 16);
+        base += total;
+    }
+    if (TOP)
+        for (int i = tid; i < win; i += kThreads) s_cut[i] = kNoKey;
+    if (tid == 0) s_next = t0 + kWaves;
+    __syncthreads();
+
+    // 1. Chunks: wave w starts with chunk t0 + w, then takes the next untaken one.
+    int t = t0 + wave;
+    if (t >= t1) return;                       // no barrier follows
+    constexpr int E = Fmt<BF16>::E;
+    const int V = P.V, k = P.k, full = V / E;  // whole vectors of a row
+    auto row_of = [&](int s) -> const char * {
+        const int r = s / L, j = s - r * L;
+        return P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
+    };
+    auto whole = [&](int c) { return min(max(full - c * kCH, 0), kCH); };
+    // lane i holds the wave's i-th pending record: a store between loads would hold every later load
+    // back until it completed, so records leave 64 at a time
+    float4 pend = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int pend_at = 0, npend = 0;
+    Best best = {kNoKey, 0, kNoKey};
+    int q = uni(t / NC), c = t - q * NC;
+    int slot = uni(s_id[q - q_lo]);
+    const char *row = row_of(slot);
+    u32x4 raw[kVPL];
+    issue_chunk<BF16>(raw, row, c * kCH, whole(c));
+    while (true) {
+        int tn = 0;
+        if (lane == 0) tn = atomicAdd(&s_next, 1);
+        tn = uni(tn);
+        const int vb = c * kCH;
+        float x[kVPL][E];
+        widen<BF16>(raw, x, row, vb, min(kCH, P.NV - vb), whole(c), V);
+        const int at = slot * NC + c, qi = q - q_lo;
+        const bool more = tn < t1;
+        const int qn = more ? uni(tn / NC) : -1, cn = tn - qn * NC;
+        if (more) {
+            if (qn != q) {
+                slot = uni(s_id[qn - q_lo]);
+                row = row_of(slot);
+            }
+            issue_chunk<BF16>(raw, row, cn * kCH, whole(cn));
+        }
+        float vm[kVPL];
+#pragma unroll
+        for (int kk = 0; kk < kVPL; ++kk) {
+            float a = x[kk][0];
+#pragma unroll
+            for (int e = 1; e < E; ++e) a = fmaxf(a, x[kk][e]);
+            vm[kk] = a;
+        }
+        float lm = vm[0];
+#pragma unroll
+        for (int kk = 1; kk < kVPL; ++kk) lm = fmaxf(lm, vm[kk]);
+        const float m = red_max_bc(lm);
+
+        int listed = 0;
+        if (TOP) {
+            // elements equal to another wave's k-th best may still win by their column
+            const int shared = __atomic_load_n(&s_cut[qi], __ATOMIC_RELAXED);
+            int floor = max(best.cut, uni(shared) == kNoKey ? kNoKey : uni(shared) - 1);
+            const int lk = order_key(lm);
+            if (__ballot(lk > floor) != 0) {
+                if (floor == kNoKey) floor = kth_floor(lk, k);
+                offer<E>(best, floor, x, vm, vb, V, k);
+                if (best.cut > uni(shared) && lane == 0) atomicMax(&s_cut[qi], best.cut);
+            }
+            if (qn != q) {                     // the wave's last chunk of this slot: its list leaves
+                listed = __popcll(__ballot(best.key != kNoKey && lane < k));
+                if (lane < listed) P.cand[(int64_t)at * k + lane] = make_int2(best.key, best.col);
+                best = {kNoKey, 0, kNoKey};
+            }
+        }
+
+        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, w4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float s = 0.0f, w = 0.0f;
+        if (fabsf(m) <= kNearMax) {
+            const float nml = -m * kLog2e;
+#pragma unroll
+            for (int kk = 0; kk < kVPL; ++kk) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float y = fmaf(x[kk][e], kLog2e, nml);
+                    const float p = __builtin_amdgcn_exp2f(y);
+                    s4[e % 4] += p;
+                    if (ENT) w4[e % 4] = fmaf(p, fmaxf(y, kFarBelow), w4[e % 4]);
+                }
+            }
+            const float r = fmaf(m, kLog2e, nml);          // what rounding nml added to every y
+            const float back = __builtin_amdgcn_exp2f(-r);
+            const float s1 = red_sum_bc((s4[0] + s4[1]) + (s4[2] + s4[3]));
+            s = s1 * back;
+            if (ENT) w = fmaf(-r, s1, red_sum_bc((w4[0] + w4[1]) + (w4[2] + w4[3]))) * back;
+        } else if (m != -INFINITY) {
+#pragma unroll
+            for (int kk = 0; kk < kVPL; ++kk) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float y = (x[kk][e] - m) * kLog2e;
+                    const float p = __builtin_amdgcn_exp2f(y);
+                    s4[e % 4] += p;
+                    if (ENT) w4[e % 4] = fmaf(p, fmaxf(y, kFarBelow), w4[e % 4]);
+                }
+            }
+            s = red_sum_bc((s4[0] + s4[1]) + (s4[2] + s4[3]));
+            if (ENT) w = red_sum_bc((w4[0] + w4[1]) + (w4[2] + w4[3]));
+        }
+        if (lane == npend) {
+            pend = make_float4(m, s, w, __int_as_float(listed));
+            pend_at = at;
+        }
+        if (++npend == 64 || !more) {
+            if (lane < npend) P.partials[pend_at] = pend;
+            npend = 0;
+        }
+        if (!more) break;
+        q = qn;
+        c = cn;
+    }
+}
+
+// Kernel 2: one wave per selected slot.
+constexpr int kJoinWaves = 4;
+
+template <bool BF16>
+__global__ __launch_bounds__(64 * kJoinWaves) void logprob_join_kernel(LogprobParams P) {
+    const int lane = lane_id();
+    const int slot = uni(blockIdx.x * kJoinWaves + (threadIdx.x >> 6));
+    if (slot >= P.rows * P.L) return;
+    fetch_args(P.mask, P.exclude, P.partials, P.tokens, P.token_stride, P.logits, P.NC, P.k);
+    if (P.mask[slot] == 0 || (P.exclude != nullptr && P.exclude[slot] != 0)) return;
+    const int r = slot / P.L, j = slot - r * P.L, NC = P.NC, k = P.k;
+    // the given token's logit, in flight beside the records
+    int tok = -1;
+    float xt = 0.0f;
+    if (P.tokens != nullptr) {
+        tok = P.tokens[(int64_t)r * P.token_stride + j];
+        if (tok >= 0 && tok < P.V) {
+            const char *row = P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
+            xt = BF16 ? __uint_as_float((uint32_t)((const uint16_t *)row)[tok] << 16) : ((const float *)row)[tok];
+        }
+    }
+    const float4 *rec = P.partials + (int64_t)slot * NC;
+    // each lane its records in order, then the lanes by a fixed tree
+    float m = -INFINITY, s = 0.0f, w = 0.0f;
+    for (int c = lane; c < NC; c += 64) {
+        const float4 p = rec[c];
+        const float mm = fmaxf(m, p.x);
+        if (mm == -INFINITY) continue;
+        const float da = fmaxf((m - mm) * kLog2e, kFarBelow), db = fmaxf((p.x - mm) * kLog2e, kFarBelow);
+        const float ea = __builtin_amdgcn_exp2f(da), eb = __builtin_amdgcn_exp2f(db);
+        w = ea * fmaf(da, s, w) + eb * fmaf(db, p.y, p.z);
+        s = ea * s + eb * p.y;
+        m = mm;
+    }
+    const float mw = red_max_bc(m);
+    const float d = mw == -INFINITY ? 0.0f : fmaxf((m - mw) * kLog2e, kFarBelow);
+    const float sc = __builtin_amdgcn_exp2f(d);
+    w = red_sum_bc(sc * fmaf(d, s, w));
+    s = red_sum_bc(sc * s);
+    // a row without a finite logit has s = 0: log s = -inf, and -inf - -inf is the NaN reported
+    const float ls = logf(s);
+    if (lane == 0) {
+        if (P.logprob != nullptr) {
+            const bool ok = tok >= 0 && tok < P.V;
+            if (!ok) {
+                set_status(P.status, DLLM_ERR_ARG);
+                ((uint32_t *)P.logprob)[slot] = 0x7FC00000u;
+            } else {
+                P.logprob[slot] = (xt - mw) - ls;
+            }
+        }
+        if (P.entropy != nullptr) P.entropy[slot] = fmaf(-kLn2, w / s, ls);
+        if (P.stats != nullptr) P.stats[slot] = make_float2(mw, ls);
+    }
+    if (k == 0) return;
+
+    // candidate lists: 64 / k of them side by side, their entries in lane order.  A wave's list may
+    // span chunks that interleave with another's, so equals are ordered by column here.
+    const int2 *cand = P.cand + (int64_t)slot * NC * k;
+    Best b = {kNoKey, 0x7FFFFFFF, kNoKey};
+    const int side = 64 / k;
+    const int li = lane / k, le = lane - li * k;
+    for (int c0 = 0; c0 < NC; c0 += side) {
+        const int c = c0 + li;
+        int key = kNoKey, col = 0;
+        if (li < side && c < NC && le < __float_as_int(rec[c].w)) {
+            const int2 e = cand[(int64_t)c * k + le];
+            key = e.x;
+            col = e.y;
+        }
+        int cut_col = __builtin_amdgcn_readlane(b.col, k - 1);
+        uint64_t in = __ballot(key != kNoKey && (key > b.cut || (key == b.cut && col < cut_col)));
+        while (in != 0) {
+            const int l = __builtin_ctzll(in);
+            const int nk = __builtin_amdgcn_readlane(key, l), nc = __builtin_amdgcn_readlane(col, l);
+            insert_at(b, __popcll(__ballot(b.key > nk || (b.key == nk && b.col < nc))), nk, nc, k);
+            cut_col = __builtin_amdgcn_readlane(b.col, k - 1);
+            in &= in - 1;
+            in &= __ballot(key > b.cut || (key == b.cut && col < cut_col));
+        }
+    }
+    if (lane < k) {
+        P.top_ids[(int64_t)slot * k + lane] = b.col;
+        P.top_lp[(int64_t)slot * k + lane] = (key_value(b.key) - mw) - ls;
+    }
+}
+
+// ---- gradient -------------------------------------------------------------------------------------
+// d/dx_v of gl * logprob + gh * entropy = gl (v == token) - p_v (gl + gh (log p_v + entropy)), with
+// p_v = exp(x_v - m - log S) from the forward's statistics: one read of the selected slots' logits
+// and one write of every slot's gradient (zeros where a slot is not selected).  Elementwise, bound
+// by HBM; per element an unpack, a subtraction, an FMA, v_exp, a multiplication (with entropy also a
+// max and an FMA) and half a pack.  A thread reads its vectors before it writes them, so the gradient
+// may replace the logits in place.
+struct GradParams {
+    const char *logits;
+    int64_t pos_stride_b, row_stride_b;
+    char *grad;
+    int64_t gpos_stride_b, grow_stride_b;
+    int32_t L, V, NV, nseg;
+    const uint8_t *mask, *exclude;
+    const int32_t *tokens;
+    int64_t token_stride;
+    const float2 *stats;
+    const float *gl, *entropy, *gh;
+    int32_t *status;
+};
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;                   // vectors per thread
+
+template <bool BF16, bool ENT>
+__global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(GradParams P) {
+    typedef typename Row<BF16>::vec vec;
+    constexpr int E = Fmt<BF16>::E;
+    fetch_args(P.logits, P.grad, P.mask, P.exclude, P.tokens, P.stats, P.gl, P.V, P.NV);
+    const int slot = blockIdx.x / P.nseg, seg = blockIdx.x - slot * P.nseg;
+    const int r = slot / P.L, j = slot - r * P.L, V = P.V;
+    char *out = P.grad + (int64_t)r * P.grow_stride_b + (int64_t)j * P.gpos_stride_b;
+    const int v0 = seg * kGradThreads * kGradVecs + threadIdx.x;
+    const int full = V / E;
+    const bool on = P.mask[slot] != 0 && (P.exclude == nullptr || P.exclude[slot] == 0);
+    if (!on) {
+        const u32x4 z = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const int v = v0 + i * kGradThreads;
+            if (v < full) {
+                __builtin_nontemporal_store(z, (vec *)out + v);
+            } else if (v < P.NV) {
+                for (int e = v * E; e < V; ++e) {
+                    if (BF16) ((uint16_t *)out)[e] = 0;
+                    else ((float *)out)[e] = 0.0f;
+                }
+            }
+        }
+        return;
+    }
+    const char *row = P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
+    u32x4 raw[kGradVecs];
+#pragma unroll
+    for (int i = 0; i < kGradVecs; ++i) {
+        const int v = v0 + i * kGradThreads;
+        if (v < full) raw[i] = __builtin_nontemporal_load((const vec *)row + v);
+    }
+    int tok = -1;
+    float gl = 0.0f;
+    if (P.tokens != nullptr) {
+        tok = P.tokens[(int64_t)r * P.token_stride + j];
+        gl = P.gl[slot];
+        if (tok < 0 || tok >= V) {             // no such token: no logprob gradient
+            tok = -1;
+            gl = 0.0f;
+            if (seg == 0 && threadIdx.x == 0) set_status(P.status, DLLM_ERR_ARG);
+        }
+    }
+    const float2 st = P.stats[slot];
+    const float nls = -st.y * kLog2e;
+    float a = gl, b = 0.0f;
+    if (ENT) {
+        const float gh = P.gh[slot];
+        a = fmaf(gh, P.entropy[slot], gl);
+        b = gh * kLn2;
+    }
+#pragma unroll
+    for (int i = 0; i < kGradVecs; ++i) {
+        const int v = v0 + i * kGradThreads;
+        if (v >= P.NV) continue;
+        float x[E], g[E];
+        if (v < full) unpack<BF16>(raw[i], x);
+        else load_vec_elems<BF16>(row, v, V, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float y = fmaf(x[e] - st.x, kLog2e, nls);
+            const float p = __builtin_amdgcn_exp2f(y);
+            g[e] = ENT ? -p * fmaf(fmaxf(y, kFarBelow), b, a) : -p * a;
+        }
+        if (tok >= 0 && tok / E == v) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) g[e] += tok - v * E == e ? gl : 0.0f;
+        }
+        if (v < full) {
+            u32x4 o;
+            if (BF16) {
+                o = u32x4{pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[E - 4], g[E - 3]), pack_bf16(g[E - 2], g[E - 1])};
+            } else {
+                o = u32x4{__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3])};
+            }
+            __builtin_nontemporal_store(o, (vec *)out + v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (v * E + e < V) {
+                    if (BF16) ((uint16_t *)out)[v * E + e] = (uint16_t)pack_bf16(g[e], 0.0f);
+                    else ((float *)out)[v * E + e] = g[e];
+                }
+            }
+        }
+    }
+}
+
+// ---- host -----------------------------------------------------------------------------------------
+// Records and candidate lists of a workspace, each part 256-byte aligned.
+bool workspace_of(int32_t rows, int32_t L, int32_t V, int32_t k, int32_t dtype, int &NV, int &NC, size_t &records,
+                  size_t &total) {
+    if (k < 0 || k > DLLM_MAX_TOP || !shape_of(rows, L, V, dtype, NV, NC, records)) return false;
+    const size_t lists = ((size_t)rows * (size_t)L * (size_t)NC * (size_t)k * sizeof(int2) + 255) & ~(size_t)255;
+    total = records + lists;
+    return true;
+}
+
+// Argument checks the two entry points share.
+dllm_status check_box(const char *who, const void *logits, int32_t dtype, int64_t pos_stride, int64_t row_stride,
+                      int32_t rows, int32_t L, int32_t V, const uint8_t *mask, const int32_t *tokens,
+                      int64_t token_stride, const int32_t *status) {
+    if (dtype != DLLM_FP32 && dtype != DLLM_BF16) return fail(DLLM_ERR_DTYPE, "%s: unknown dtype %d", who, (int)dtype);
+    if (rows < 0) return fail(DLLM_ERR_ARG, "%s: rows < 0", who);
+    if (L < 1 || L > DLLM_MAX_L) return fail(DLLM_ERR_SHAPE, "%s: L=%d outside [1, %d]", who, L, DLLM_MAX_L);
+    if (V < 1) return fail(DLLM_ERR_ARG, "%s: V < 1", who);
+    if (V > 1 << 30) return fail(DLLM_ERR_SHAPE, "%s: V=%d > 2^30", who, V);   // columns plus a chunk stay in 32 bits
+    if (rows > DLLM_MAX_ROWS || (int64_t)rows * L > DLLM_MAX_POSITIONS)
+        return fail(DLLM_ERR_SHAPE, "%s: rows=%d, L=%d exceed the limits", who, rows, L);
+    const int64_t nv = ((int64_t)V + (dtype == DLLM_BF16 ? 7 : 3)) / (dtype == DLLM_BF16 ? 8 : 4);
+    if ((int64_t)rows * L * ((nv + kCH - 1) / kCH) >= (int64_t)1 << 31)
+        return fail(DLLM_ERR_SHAPE, "%s: rows*L*chunks too large", who);
+    if (pos_stride < V || row_stride < (int64_t)L * pos_stride)
+        return fail(DLLM_ERR_ARG, "%s: strides too small (pos %lld, row %lld)", who, (long long)pos_stride,
+                    (long long)row_stride);
+    if (tokens && token_stride < L)
+        return fail(DLLM_ERR_ARG, "%s: token stride %lld < L", who, (long long)token_stride);
+    if (rows > 0 && (!logits || !mask || !status)) return fail(DLLM_ERR_ARG, "%s: null required pointer", who);
+    if (((uintptr_t)logits & (dtype == DLLM_BF16 ? 1 : 3)) != 0)
+        return fail(DLLM_ERR_ARG, "%s: logits not aligned to their type", who);
+    return DLLM_OK;
+}
+
+}  // namespace
+
+extern "C" size_t dllm_logprobs_workspace_bytes(int32_t rows, int32_t L, int32_t V, int32_t k, int32_t dtype) {
+    int NV, NC;
+    size_t records, total;
+    return workspace_of(rows, L, V, k, dtype, NV, NC, records, total) ? total : 0;
+}
+
+extern "C" dllm_status dllm_logprobs(void *stream, const void *logits, int32_t dtype, int64_t pos_stride,
+                                     int64_t row_stride, int32_t rows, int32_t L, int32_t V, const uint8_t *mask,
+                                     const uint8_t *exclude, const int32_t *tokens, int64_t token_stride, int32_t k,
+                                     float *logprob, float *entropy, float *stats, int32_t *top_ids,
+                                     float *top_logprobs, void *workspace, size_t workspace_bytes, int32_t *status) {
+    const char *who = "dllm_logprobs";
+    dllm_status rc = check_box(who, logits, dtype, pos_stride, row_stride, rows, L, V, mask, tokens, token_stride, status);
+    if (rc != DLLM_OK) return rc;
+    if (k < 0 || k > DLLM_MAX_TOP || k > V)
+        return fail(DLLM_ERR_ARG, "%s: k=%d outside [0, min(%d, V)]", who, k, DLLM_MAX_TOP);
+    if (rows == 0) return DLLM_OK;
+    if ((tokens == nullptr) != (logprob == nullptr))
+        return fail(DLLM_ERR_ARG, "%s: tokens and logprob must be both given or both NULL", who);
+    if (k > 0 && (!top_ids || !top_logprobs)) return fail(DLLM_ERR_ARG, "%s: k=%d without top_ids and top_logprobs", who, k);
+    if (!logprob && !entropy && !stats && k == 0) return fail(DLLM_ERR_ARG, "%s: nothing to compute", who);
+    if (((uintptr_t)stats & 7) != 0) return fail(DLLM_ERR_ARG, "%s: stats not 8-byte aligned", who);
+    LogprobParams P{};
+    size_t records, need;
+    workspace_of(rows, L, V, k, dtype, P.NV, P.NC, records, need);
+    if (!workspace) return fail(DLLM_ERR_ARG, "%s: null workspace", who);
+    if (workspace_bytes < need) return fail(DLLM_ERR_ARG, "%s: workspace %zu bytes < %zu needed", who, workspace_bytes, need);
+    if (((uintptr_t)workspace & 15) != 0) return fail(DLLM_ERR_ARG, "%s: workspace not 16-byte aligned", who);
+    const int es = dtype == DLLM_BF16 ? 2 : 4;
+    P.logits = (const char *)logits;
+    P.pos_stride_b = pos_stride * es;
+    P.row_stride_b = row_stride * es;
+    P.rows = rows; P.L = L; P.V = V; P.k = k;
+    P.mask = mask; P.exclude = exclude;
+    P.tokens = tokens; P.token_stride = token_stride;
+    P.logprob = logprob; P.entropy = entropy; P.stats = (float2 *)stats;
+    P.top_ids = top_ids; P.top_lp = top_logprobs;
+    P.partials = (float4 *)workspace;
+    P.cand = (int2 *)((char *)workspace + records);
+    P.status = status;
+
+    // The scoring kernel's grid rule: the same chunks per workgroup, the same measured thresholds.
+    const hipStream_t st = (hipStream_t)stream;
+    const int64_t S = (int64_t)rows * L, cus = cu_count(), boxed = S * P.NC;
+    int64_t grid = cus * (boxed < cus * kTinyBoxChunksPerCU ? 1 : boxed < cus * kSmallBoxChunksPerCU ? 2 : kGroupsPerCU);
+    grid = grid < (S + 2047) / 2048 ? (S + 2047) / 2048 : grid;
+    const int64_t most = (boxed + kWaves - 1) / kWaves;
+    grid = grid > most ? most : grid;
+    const int64_t per = (boxed + grid - 1) / grid;
+    const int win = (int)((per + P.NC - 1) / P.NC + 2);
+    const size_t lds = (size_t)win * sizeof(int) * (k > 0 ? 2 : 1);
+    const bool bf = dtype == DLLM_BF16, ent = entropy != nullptr;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, st, P, win); };
+    if (bf) {
+        if (k > 0) ent ? go(logprob_chunks_kernel<true, true, true>) : go(logprob_chunks_kernel<true, false, true>);
+        else ent ? go(logprob_chunks_kernel<true, true, false>) : go(logprob_chunks_kernel<true, false, false>);
+    } else {
+        if (k > 0) ent ? go(logprob_chunks_kernel<false, true, true>) : go(logprob_chunks_kernel<false, false, true>);
+        else ent ? go(logprob_chunks_kernel<false, true, false>) : go(logprob_chunks_kernel<false, false, false>);
+    }
+    rc = check_hip(hipGetLastError(), "dllm_logprobs chunks launch");
+    if (rc != DLLM_OK) return rc;
+    const dim3 jg((unsigned)((S + kJoinWaves - 1) / kJoinWaves)), jb(64 * kJoinWaves);
+    if (bf) hipLaunchKernelGGL(logprob_join_kernel<true>, jg, jb, 0, st, P);
+    else hipLaunchKernelGGL(logprob_join_kernel<false>, jg, jb, 0, st, P);
+    return check_hip(hipGetLastError(), "dllm_logprobs join launch");
+}
+
+extern "C" dllm_status dllm_logprobs_grad(void *stream, const void *logits, int32_t dtype, int64_t pos_stride,
+                                          int64_t row_stride, int32_t rows, int32_t L, int32_t V, const uint8_t *mask,
+                                          const uint8_t *exclude, const int32_t *tokens, int64_t token_stride,
+                                          const float *stats, const float *grad_logprob, const float *entropy,
+                                          const float *grad_entropy, void *grad_logits, int64_t grad_pos_stride,
+                                          int64_t grad_row_stride, int32_t *status) {
+    const char *who = "dllm_logprobs_grad";
+    dllm_status rc = check_box(who, logits, dtype, pos_stride, row_stride, rows, L, V, mask, tokens, token_stride, status);
+    if (rc != DLLM_OK) return rc;
+    if (grad_pos_stride < V || grad_row_stride < (int64_t)L * grad_pos_stride)
+        return fail(DLLM_ERR_ARG, "%s: gradient strides too small (pos %lld, row %lld)", who, (long long)grad_pos_stride,
+                    (long long)grad_row_stride);
+    if (rows == 0) return DLLM_OK;
+    if (!stats || !grad_logits) return fail(DLLM_ERR_ARG, "%s: null required pointer", who);
+    if ((tokens == nullptr) != (grad_logprob == nullptr))
+        return fail(DLLM_ERR_ARG, "%s: tokens and grad_logprob must be both given or both NULL", who);
+    if (grad_entropy && !entropy) return fail(DLLM_ERR_ARG, "%s: grad_entropy without the forward's entropy", who);
+    if (!grad_logprob && !grad_entropy) return fail(DLLM_ERR_ARG, "%s: no gradient given", who);
+    if (((uintptr_t)stats & 7) != 0) return fail(DLLM_ERR_ARG, "%s: stats not 8-byte aligned", who);
+    const int es = dtype == DLLM_BF16 ? 2 : 4;
+    if (((uintptr_t)grad_logits & (es - 1)) != 0) return fail(DLLM_ERR_ARG, "%s: grad_logits not aligned to their type", who);
+    const uintptr_t a = (uintptr_t)logits, b = (uintptr_t)grad_logits;
+    const uintptr_t an = (((uintptr_t)(rows - 1) * row_stride) + (uintptr_t)(L - 1) * pos_stride + V) * es;
+    const uintptr_t bn = (((uintptr_t)(rows - 1) * grad_row_stride) + (uintptr_t)(L - 1) * grad_pos_stride + V) * es;
+    if (a < b + bn && b < a + an && !(a == b && pos_stride == grad_pos_stride && row_stride == grad_row_stride))
+        return fail(DLLM_ERR_ARG, "%s: grad_logits overlaps logits without being it", who);
+    GradParams P{};
+    P.logits = (const char *)logits;
+    P.pos_stride_b = pos_stride * es;
+    P.row_stride_b = row_stride * es;
+    P.grad = (char *)grad_logits;
+    P.gpos_stride_b = grad_pos_stride * es;
+    P.grow_stride_b = grad_row_stride * es;
+    P.L = L; P.V = V;
+    P.NV = (int)(((int64_t)V + 16 / es - 1) / (16 / es));
+    P.nseg = (P.NV + kGradThreads * kGradVecs - 1) / (kGradThreads * kGradVecs);
+    P.mask = mask; P.exclude = exclude;
+    P.tokens = tokens; P.token_stride = token_stride;
+    P.stats = (const float2 *)stats;
+    P.gl = grad_logprob; P.entropy = entropy; P.gh = grad_entropy;
+    P.status = status;
+    const int64_t blocks = (int64_t)rows * L * P.nseg;
+    if (blocks >= (int64_t)1 << 31) return fail(DLLM_ERR_SHAPE, "%s: rows*L*V too large", who);
+    const dim3 grid((unsigned)blocks), block(kGradThreads);
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == DLLM_BF16) {
+        if (grad_entropy) hipLaunchKernelGGL((logprob_grad_kernel<true, true>), grid, block, 0, st, P);
+        else hipLaunchKernelGGL((logprob_grad_kernel<true, false>), grid, block, 0, st, P);
+    } else {
+        if (grad_entropy) hipLaunchKernelGGL((logprob_grad_kernel<false, true>), grid, block, 0, st, P);
+        else hipLaunchKernelGGL((logprob_grad_kernel<false, false>), grid, block, 0, st, P);
+    }
+    return check_hip(hipGetLastError(), "dllm_logprobs_grad launch");
+}

@@ -49,6 +49,10 @@ typedef enum { DLLM_FP32 = 0, DLLM_BF16 = 1 } dllm_dtype;
 #define DLLM_MAX_POSITIONS 262144  /* rows * L */
 #define DLLM_MAX_QUEUE 8192        /* queue capacity */
 #define DLLM_MAX_SHARDS 1024       /* vocabulary shards */
+#define DLLM_MAX_TOP 32            /* alternatives per slot */
+#define DLLM_MAX_TOKENS (1 << 24)  /* columns of a box (rows * W) for the embedding calls */
+#define DLLM_MAX_VOCAB (1 << 24)   /* rows of an embedding table */
+#define DLLM_MAX_WIDTH (1 << 20)   /* columns of an embedding table */
 
 /* Request table, indexed by request id ([BlockServe] §II-A: prompt length p_i, K_i = ceil(g_i/L)
  * blocks, current block index b_i).  All arrays are device memory of length n_req (blk_mask:
@@ -344,6 +348,109 @@ dllm_status dllm_compact(void *stream, int32_t rows, int32_t L, int32_t W, int32
                          const uint8_t *done, int32_t *row_req, int32_t rows_cap,
                          const dllm_reqs *reqs, const dllm_queue *queue, int64_t budget,
                          dllm_meta *meta, int32_t *status);
+
+/* dllm_logprobs — log probabilities of given tokens at selected slots of the box's logits, with the
+ * entropy of the distribution and its top alternatives: what a served answer reports beside its
+ * tokens, and the forward half of a masked-token loss.
+ *
+ * The distribution is the softmax whose largest probability dllm_step uses as confidence
+ * ([DiLaServe] §三 3.1).  A slot (r, j) is selected when mask[r, j] != 0 and exclude is NULL or
+ * exclude[r, j] == 0: with mask = the step's mask_in and exclude = its mask_out these are exactly the
+ * slots the step unmasked, and tokens = input_ids + W - L (token_stride W) the tokens it wrote.  For
+ * every selected slot, with x its V logits, m = max x and S = sum_v exp(x_v - m):
+ *   logprob[r, j]        = x_t - m - log S for t = tokens[r*token_stride + j];
+ *   entropy[r, j]        = -sum_v p_v log p_v (natural logarithm), p_v = exp(x_v - m) / S;
+ *   stats[r, j, 0..1]    = m, log S (what dllm_logprobs_grad reads);
+ *   top_ids[r, j, 0..k-1] = the k columns with the largest x, the lowest column first among equal
+ *                          values; top_logprobs the log probability of each.
+ * Arithmetic is float32 and independent of timing and of the rest of the batch, bit for bit.
+ * Slots that are not selected are neither read nor written: a caller may let the outputs of
+ * successive steps accumulate in one array.  tokens may be the step's input_ids (nothing is written
+ * there).
+ *
+ * Logits are as for dllm_step, but may hold -inf (a column that cannot be chosen: probability 0, log
+ * probability -inf, no part in the entropy) and need no alignment beyond their type.  A slot whose
+ * logits are all -inf, or hold NaN or +inf, reports NaN for every log probability and the entropy; if
+ * it holds NaN, the order of its alternatives is not specified.  A token outside [0, V) sets
+ * *status = DLLM_ERR_ARG and its logprob reads NaN.
+ * tokens with logprob, entropy, stats, and top_ids with top_logprobs (k > 0) are optional, at least
+ * one of them given.  0 <= k <= min(DLLM_MAX_TOP, V).  stats 8-byte aligned.
+ * workspace: dllm_logprobs_workspace_bytes(rows, L, V, k, dtype) bytes, 16-byte aligned, any contents;
+ * not shared by overlapping calls.  Outputs must not overlap the inputs or the workspace.
+ * Errors: those of dllm_step for logits, shape, strides and workspace, and DLLM_ERR_SHAPE for V > 2^30;
+ * DLLM_ERR_ARG for k out of
+ * range, token_stride < L, logits not aligned to their type, tokens without logprob or the reverse,
+ * k > 0 without its outputs, or nothing to compute.  rows == 0 is a no-op.  Work: two kernels. */
+size_t dllm_logprobs_workspace_bytes(int32_t rows, int32_t L, int32_t V, int32_t k, int32_t dtype);
+dllm_status dllm_logprobs(void *stream, const void *logits, int32_t dtype, int64_t pos_stride,
+                          int64_t row_stride, int32_t rows, int32_t L, int32_t V, const uint8_t *mask,
+                          const uint8_t *exclude, const int32_t *tokens, int64_t token_stride, int32_t k,
+                          float *logprob, float *entropy, float *stats, int32_t *top_ids,
+                          float *top_logprobs, void *workspace, size_t workspace_bytes, int32_t *status);
+
+/* dllm_logprobs_grad — the gradient of dllm_logprobs' outputs with respect to the logits.
+ *
+ * For every selected slot, with p_v = exp(x_v - stats[0] - stats[1]), gl = grad_logprob[r, j], gh =
+ * grad_entropy[r, j] and H = entropy[r, j]:
+ *   grad_logits[r, j, v] = gl ((v == token) - p_v) - gh p_v (log p_v + H),
+ * computed in float32 and rounded once to the logits' type; columns with x = -inf get 0.  Every slot
+ * that is not selected is written as zeros; columns past V of a strided row are left alone.
+ * stats and entropy are the forward's outputs for the same logits (entropy may be NULL without
+ * grad_entropy).  tokens with grad_logprob, and grad_entropy, are optional, at least one given.
+ * grad_logits has the logits' type and strides of its own (in elements); it may be the logits
+ * themselves (same address and strides: the gradient replaces them) but must not overlap them
+ * otherwise.  A token outside [0, V) sets *status = DLLM_ERR_ARG and contributes no log-probability
+ * gradient.  A slot with NaN statistics gets NaN.
+ * Errors: as dllm_logprobs (there is no workspace), plus DLLM_ERR_ARG for gradient strides too small
+ * or a partial overlap, and DLLM_ERR_SHAPE when rows*L*V needs 2^31 workgroups.  rows == 0 is a no-op.
+ * Work: one kernel. */
+dllm_status dllm_logprobs_grad(void *stream, const void *logits, int32_t dtype, int64_t pos_stride,
+                               int64_t row_stride, int32_t rows, int32_t L, int32_t V, const uint8_t *mask,
+                               const uint8_t *exclude, const int32_t *tokens, int64_t token_stride,
+                               const float *stats, const float *grad_logprob, const float *entropy,
+                               const float *grad_entropy, void *grad_logits, int64_t grad_pos_stride,
+                               int64_t grad_row_stride, int32_t *status);
+
+/* dllm_embed — the packed box's token ids to scaled embedding rows: the input of the forward that
+ * follows dllm_pack ([BlockServe] §II-E: the dense left-padded box; padding contributes nothing).
+ *
+ * For n < n_tokens: out[n, 0..D-1] = scale * table[ids[n], 0..D-1], computed in float32 and rounded
+ * once to the output's type; a row of zeros where valid is given and valid[n] == 0 (the id is then
+ * not looked at).  An id outside [0, n_vocab) sets *status = DLLM_ERR_ARG and its row is zeros.
+ * ids, valid: box_ids and box_valid as dllm_pack writes them (n_tokens = rows * W), or any int32 /
+ * uint8 arrays; valid may be NULL.  table: [n_vocab, D], out: [n_tokens, D], fp32 or bf16 each, rows
+ * table_stride / out_stride elements apart, aligned to their types.  out must not overlap the inputs.
+ * Errors: DLLM_ERR_ARG (null required pointer, n_tokens < 0, stride < D, misaligned),
+ * DLLM_ERR_SHAPE (n_tokens > DLLM_MAX_TOKENS, n_vocab outside [1, DLLM_MAX_VOCAB], D outside
+ * [1, DLLM_MAX_WIDTH]), DLLM_ERR_DTYPE.  n_tokens == 0 is a no-op.  Work: one kernel. */
+dllm_status dllm_embed(void *stream, const void *table, int32_t table_dtype, int64_t table_stride,
+                       int32_t n_vocab, int32_t D, const int32_t *ids, const uint8_t *valid,
+                       int32_t n_tokens, float scale, void *out, int32_t out_dtype, int64_t out_stride,
+                       int32_t *status);
+
+/* dllm_embed_grad — the gradient of dllm_embed with respect to the table.
+ *
+ * For v < n_vocab, over the tokens n with ids[n] == v (and valid[n] != 0 when valid is given):
+ *   grad_table[v, :] = scale * sum_n grad_out[n, :]                    (accumulate == 0: every row written,
+ *                                                                       zeros where v does not occur);
+ *   grad_table[v, :] += scale * sum_n grad_out[n, :]                   (accumulate != 0: rows whose v does
+ *                                                                       not occur are left alone).
+ * Sums are float32 in an order fixed by the ids alone (tokens sorted by id, then position), so the
+ * result's bits do not depend on timing; each row is rounded once to the table gradient's type.  An id
+ * outside [0, n_vocab) sets *status = DLLM_ERR_ARG and contributes nothing.  One id may hold any share
+ * of the tokens (the mask token of a training box holds a large one).
+ * grad_out: [n_tokens, D], grad_table: [n_vocab, D], fp32 or bf16 each, with row strides; columns past
+ * D are left alone.  workspace: dllm_embed_grad_workspace_bytes(n_tokens, n_vocab, D) bytes, 256-byte
+ * aligned, any contents; not shared by overlapping calls.  grad_table and workspace must not overlap
+ * the inputs or each other.
+ * Errors: as dllm_embed, plus DLLM_ERR_ARG for the workspace.  n_tokens == 0 with accumulate is a
+ * no-op; without, it writes zeros. */
+size_t dllm_embed_grad_workspace_bytes(int32_t n_tokens, int32_t n_vocab, int32_t D);
+dllm_status dllm_embed_grad(void *stream, const void *grad_out, int32_t grad_dtype, int64_t grad_stride,
+                            const int32_t *ids, const uint8_t *valid, int32_t n_tokens, float scale,
+                            int32_t n_vocab, int32_t D, void *grad_table, int32_t table_dtype,
+                            int64_t table_stride, int32_t accumulate, void *workspace,
+                            size_t workspace_bytes, int32_t *status);
 
 /* Text for the last non-OK status returned on the calling host thread ("" if none). */
 const char *dllm_last_error(void);
