@@ -316,22 +316,33 @@ def dllm_step_features(rows, L, row_req, reqs: "ReqTable", conf, mask_out, featu
 
 def _call(fn, where, stream, tensors, *args):
     """fn(stream, *args) on the device that all `tensors` share (None entries aside), whatever the
-    current device is; `stream`, when given, must be that device's."""
-    dev = None
+    current device is; `stream`, when given, must be that device's.  The small calls take
+    microseconds on the device, so this path avoids building stream objects."""
+    dev = -1
     for t in tensors:
         if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"{where}: tensors on {dev} and {t.device}; all must be on one device")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"{where}: stream of {stream.device} for tensors on {dev}")
-    if dev.index == torch.cuda.current_device():
-        rc = fn(_stream(stream), *args)
+            d = t.get_device()
+            if dev < 0:
+                dev = d
+            elif d != dev:
+                raise ValueError(f"{where}: tensors on devices {dev} and {d}; all must be on one device")
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"{where}: stream of {stream.device} for tensors on device {dev}")
+        handle = stream.cuda_stream
+    else:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch.cuda.current_device():
+        rc = fn(handle, *args)
     else:
         with torch.cuda.device(dev):
-            rc = fn(_stream(stream), *args)
-    _lib.check(rc, where)
+            rc = fn(handle, *args)
+    if rc != 0:
+        _lib.check(rc, where)
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _tokens_arg(tokens, rows, L):
@@ -386,9 +397,9 @@ def dllm_logprobs(logits, mask, tokens, logprob, workspace, status, entropy=None
             _need(t, dt, nm, n)
     _call(_lib.lib().dllm_logprobs, "dllm_logprobs", stream,
           (logits, mask, exclude, tokens, logprob, entropy, stats, top_ids, top_logprobs, workspace, status),
-          _ptr(logits), _DT[logits.dtype], pos_stride, row_stride, rows, L, V, _ptr(mask), _ptr(exclude), _ptr(tokens),
-          token_stride, int(k), _ptr(logprob), _ptr(entropy), _ptr(stats), _ptr(top_ids), _ptr(top_logprobs),
-          _ptr(workspace), workspace.numel(), _ptr(status))
+          _adr(logits), _DT[logits.dtype], pos_stride, row_stride, rows, L, V, _adr(mask), _adr(exclude), _adr(tokens),
+          token_stride, int(k), _adr(logprob), _adr(entropy), _adr(stats), _adr(top_ids), _adr(top_logprobs),
+          _adr(workspace), workspace.numel(), _adr(status))
 
 
 def dllm_logprobs_grad(logits, mask, tokens, stats, grad_logprob, grad_logits, status, entropy=None, grad_entropy=None,
@@ -415,9 +426,9 @@ def dllm_logprobs_grad(logits, mask, tokens, stats, grad_logprob, grad_logits, s
             _need(t, dt, nm, rows * L)
     _call(_lib.lib().dllm_logprobs_grad, "dllm_logprobs_grad", stream,
           (logits, mask, exclude, tokens, stats, grad_logprob, entropy, grad_entropy, grad_logits, status),
-          _ptr(logits), _DT[logits.dtype], pos_stride, row_stride, rows, L, V, _ptr(mask), _ptr(exclude), _ptr(tokens),
-          token_stride, _ptr(stats), _ptr(grad_logprob), _ptr(entropy), _ptr(grad_entropy), _ptr(grad_logits),
-          grad_pos_stride, grad_row_stride, _ptr(status))
+          _adr(logits), _DT[logits.dtype], pos_stride, row_stride, rows, L, V, _adr(mask), _adr(exclude), _adr(tokens),
+          token_stride, _adr(stats), _adr(grad_logprob), _adr(entropy), _adr(grad_entropy), _adr(grad_logits),
+          grad_pos_stride, grad_row_stride, _adr(status))
 
 
 def _matrix(t, name):
@@ -458,8 +469,8 @@ def dllm_embed(table, ids, out, status, valid=None, scale=1.0, stream=None):
     if D_out != D or n_out < n:
         raise ValueError(f"out holds {n_out} rows of {D_out}, needs {n} of {D}")
     _call(_lib.lib().dllm_embed, "dllm_embed", stream, (table, ids, valid, out, status),
-          _ptr(table), _DT[table.dtype], ts, n_vocab, D, _ptr(ids), _ptr(valid), n, float(scale), _ptr(out),
-          _DT[out.dtype], os_, _ptr(status))
+          _adr(table), _DT[table.dtype], ts, n_vocab, D, _adr(ids), _adr(valid), n, float(scale), _adr(out),
+          _DT[out.dtype], os_, _adr(status))
 
 
 def dllm_embed_grad_workspace_bytes(n_tokens: int, n_vocab: int, D: int) -> int:
@@ -483,9 +494,9 @@ def dllm_embed_grad(grad_out, ids, grad_table, workspace, status, valid=None, sc
     _need(workspace, torch.uint8, "workspace")
     _call(_lib.lib().dllm_embed_grad, "dllm_embed_grad", stream,
           (grad_out, ids, valid, grad_table, workspace, status),
-          _ptr(grad_out), _DT[grad_out.dtype], gs, _ptr(ids), _ptr(valid), n, float(scale), n_vocab, D,
-          _ptr(grad_table), _DT[grad_table.dtype], ts, int(bool(accumulate)), _ptr(workspace), workspace.numel(),
-          _ptr(status))
+          _adr(grad_out), _DT[grad_out.dtype], gs, _adr(ids), _adr(valid), n, float(scale), n_vocab, D,
+          _adr(grad_table), _DT[grad_table.dtype], ts, int(bool(accumulate)), _adr(workspace), workspace.numel(),
+          _adr(status))
 
 
 class ReqTable:

@@ -18,17 +18,15 @@
 //   - y is one FMA, x*log2e - m*log2e.  The product m*log2e is rounded once per chunk; its residual r
 //     (exact, by an FMA) is taken out of the sums by a factor 2^-r, so large offsets of the logits
 //     cost no accuracy.  Chunks whose maximum lies beyond kNearMax subtract first instead.
-//   - Alternatives: each wave keeps the k best of the chunks it took from a slot sorted across its
-//     lanes (lane i holds the i-th best).  An element enters only if it beats the k-th; an insertion
-//     is a ballot, a count and one lane shift.  A wave's list starts from the k-th largest lane
-//     maximum of its first chunk (a lower bound of the k-th best, found by 16 ballots), and waves of a
-//     workgroup share the best k-th value seen per slot in LDS, so after the first chunks almost every
-//     chunk is passed over by one comparison per lane.  Elements are visited in column order and
-//     must be strictly better, which keeps the lowest column among equals; a row of equal logits
-//     costs k insertions per chunk at most.
-//   - A second kernel, one wave per slot, joins the chunk records in a fixed order, so the sums' bits
-//     do not depend on timing, merges the candidate lists under the full order (value, then column),
-//     and looks up the given token's logit.
+//   - Alternatives: while a chunk is in registers each lane's largest element is known anyway; it is
+//     kept (2 or 4 bytes per 128-byte lane share).  The k-th largest of those maxima cannot exceed the
+//     k-th largest element, so the k best lie in the few lane shares whose maximum reaches it.
+//   - A second kernel joins the chunk records in a fixed order, so the sums' bits do not depend on
+//     timing, and looks up the given token's logit.  For the alternatives it bounds the k-th best
+//     from below (the k-th largest of 64 group maxima, by ballots), reads again only the lane shares
+//     that reach the bound (about 25 of 2432 for k = 20 and V = 152064), and puts each of their
+//     elements above the bound into its place by counting the ones before it.
+//     Keeping sorted lists in the streaming kernel instead took 2.3 times as long.
 #include "elem_common.h"
 
 namespace {
@@ -51,8 +49,8 @@ struct LogprobParams {
     float2 *stats;
     int32_t *top_ids;
     float *top_lp;
-    float4 *partials;                          // [rows*L*NC] {max, sum, weighted sum, candidates listed}
-    int2 *cand;                                // [rows*L*NC*k] {key, column}
+    float4 *partials;                          // [rows*L*NC] {max, sum, weighted sum, -}
+    char *lane_max;                            // [rows*L*NC*64] each lane's largest element, in the logits' type
     int32_t *status;
 };
 
@@ -70,39 +68,43 @@ __device__ __forceinline__ uint32_t selected16(const LogprobParams &P, int s0, i
     return b;
 }
 
-// The kVPL loads of a chunk for this lane: its first nf vectors are whole; addresses past them are
-// clamped and their values replaced in widen().
+// The kVPL loads of a chunk for this lane, whose first nf vectors are whole.  A row's ragged last
+// vector, and every one past it, is read as the row's last E elements (a vector that lies in the row);
+// widen() drops what belongs to other vectors.  Rows shorter than a vector are read there by element.
 template <bool BF16>
-__device__ __forceinline__ void issue_chunk(u32x4 (&raw)[kVPL], const char *row, int vb, int nf) {
+__device__ __forceinline__ void issue_chunk(u32x4 (&raw)[kVPL], const char *row, int vb, int nf, int V) {
     typedef typename Row<BF16>::vec vec;
+    constexpr int E = Fmt<BF16>::E;
     const int lane = lane_id();
-    const vec *base = (const vec *)row + vb;
     if (nf == kCH) {
+        const vec *base = (const vec *)row + vb;
 #pragma unroll
         for (int k = 0; k < kVPL; ++k) raw[k] = __builtin_nontemporal_load(base + k * 64 + lane);
-    } else if (nf > 0) {
+    } else if (V >= E) {
 #pragma unroll
-        for (int k = 0; k < kVPL; ++k) raw[k] = __builtin_nontemporal_load(base + min(k * 64 + lane, nf - 1));
+        for (int k = 0; k < kVPL; ++k) {
+            const uint32_t at = (uint32_t)min((vb + k * 64 + lane) * E, V - E) * (16 / E);
+            raw[k] = __builtin_nontemporal_load((const vec *)(row + at));
+        }
+        asm volatile("; short chunk");         // keeps these loads apart: merged, both would hold 16 address registers
     }
 }
+// The chunk's values, in an order of their own within a lane; -inf where there is no element.
 template <bool BF16>
-__device__ __forceinline__ void widen(const u32x4 (&raw)[kVPL], float (&x)[kVPL][Fmt<BF16>::E], const char *row, int vb,
-                                      int n, int nf, int V) {
+__device__ __forceinline__ void widen(const u32x4 (&raw)[kVPL], float (&x)[kVPL][Fmt<BF16>::E], const char *row, int nf,
+                                      int V) {
+    constexpr int E = Fmt<BF16>::E;
 #pragma unroll
     for (int k = 0; k < kVPL; ++k) unpack<BF16>(raw[k], x[k]);
     if (nf < kCH) {
-        const int lane = lane_id();
+        const int lane = lane_id(), ragged = V % E;
+        if (V < E) load_vec_elems<BF16>(row, 0, V, x[0]);
 #pragma unroll
         for (int k = 0; k < kVPL; ++k) {
             const int v = k * 64 + lane;
-            if (v >= nf) {
-                if (v < n) {                   // the row's ragged last vector
-                    load_vec_elems<BF16>(row, vb + v, V, x[k]);
-                } else {
+            const int first = v < nf || (V < E && v == 0) ? 0 : v == nf ? E - ragged : E;   // elements before it are not this vector's
 #pragma unroll
-                    for (int e = 0; e < Fmt<BF16>::E; ++e) x[k][e] = -INFINITY;
-                }
-            }
+            for (int e = 0; e < E; ++e) x[k][e] = e < first ? -INFINITY : x[k][e];
         }
     }
 }
@@ -136,45 +138,10 @@ __device__ __forceinline__ int kth_floor(int key, int k) {
     return t == 0 ? kNoKey : (int)(t ^ 0x80000000u) - 1;
 }
 
-// Offer the vectors x[kk] of a chunk (column of lane l, element e: (vb + kk*64 + l)*E + e) whose
-// maximum exceeds the floor, in column order.
-template <int E>
-__device__ __forceinline__ void offer(Best &b, int floor, float (&x)[kVPL][E], float (&vm)[kVPL], int vb, int V, int k) {
-    const int lane = lane_id();
-#pragma unroll
-    for (int kk = 0; kk < kVPL; ++kk) {
-        const int vk = order_key(vm[kk]);
-        uint64_t hit = __ballot(vk > floor);
-        while (hit != 0) {
-            const int l = __builtin_ctzll(hit);
-            hit &= hit - 1;
-            // that vector's elements to lanes 0 .. E-1
-            int c = 0;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                c = lane == e ? __builtin_amdgcn_readlane(__float_as_int(x[kk][e]), l) : c;
-            const int ck = order_key(__int_as_float(c));
-            const int col0 = (vb + kk * 64 + l) * E;
-            uint64_t in = __ballot(lane < E && col0 + lane < V && ck > floor);
-            while (in != 0) {
-                const int e = __builtin_ctzll(in);
-                const int key = __builtin_amdgcn_readlane(ck, e);
-                insert_at(b, __popcll(__ballot(b.key >= key)), key, col0 + e, k);
-                floor = max(floor, b.cut);
-                in &= in - 1;
-                in &= __ballot(ck > floor);
-            }
-            hit &= __ballot(vk > floor);
-        }
-    }
-}
-
-// Kernel 1: one record per chunk of every selected slot, and the candidate lists.
+// Kernel 1: one record per chunk of every selected slot, and its lanes' maxima.
 template <bool BF16, bool ENT, bool TOP>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void logprob_chunks_kernel(LogprobParams P,
-                                                                                                          int win) {
-    extern __shared__ int s_id[];              // [win] selected slots of this workgroup's window; with TOP
-    int *s_cut = s_id + win;                   // [win] the best k-th key any wave holds for them
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void logprob_chunks_kernel(LogprobParams P) {
+    extern __shared__ int s_id[];              // [win] selected slots of this workgroup's window
     __shared__ int s_tmp[2][kWaves];
     __shared__ int s_next;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -185,7 +152,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
     // 0. Number the selected slots in slot order (16 per thread and tile), split their chunks evenly
     //    over the workgroups and list this workgroup's slots in LDS.
     const uint32_t mb0 = selected16(P, tid * 16, S);
-    fetch_args(P.logits, P.row_stride_b, P.pos_stride_b, P.partials, P.NV, P.V, P.k);
+    fetch_args(P.logits, P.row_stride_b, P.pos_stride_b, P.partials, P.lane_max, P.V);
     int more_cnt = 0;
     for (int t = 1; t < ntiles; ++t) more_cnt += __popc(selected16(P, t * kTile + tid * 16, S));
     // slots selected before this thread's 16 in its tile, and in the whole tile
@@ -229,8 +196,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
         list(mb, base + before, t * kTile + tid * 16);
         base += total;
     }
-    if (TOP)
-        for (int i = tid; i < win; i += kThreads) s_cut[i] = kNoKey;
     if (tid == 0) s_next = t0 + kWaves;
     __syncthreads();
 
@@ -238,7 +203,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
     int t = t0 + wave;
     if (t >= t1) return;                       // no barrier follows
     constexpr int E = Fmt<BF16>::E;
-    const int V = P.V, k = P.k, full = V / E;  // whole vectors of a row
+    const int V = P.V, full = V / E;           // whole vectors of a row
     auto row_of = [&](int s) -> const char * {
         const int r = s / L, j = s - r * L;
         return P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
@@ -248,20 +213,18 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
     // back until it completed, so records leave 64 at a time
     float4 pend = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     int pend_at = 0, npend = 0;
-    Best best = {kNoKey, 0, kNoKey};
     int q = uni(t / NC), c = t - q * NC;
     int slot = uni(s_id[q - q_lo]);
     const char *row = row_of(slot);
     u32x4 raw[kVPL];
-    issue_chunk<BF16>(raw, row, c * kCH, whole(c));
+    issue_chunk<BF16>(raw, row, c * kCH, whole(c), V);
     while (true) {
         int tn = 0;
         if (lane == 0) tn = atomicAdd(&s_next, 1);
         tn = uni(tn);
-        const int vb = c * kCH;
         float x[kVPL][E];
-        widen<BF16>(raw, x, row, vb, min(kCH, P.NV - vb), whole(c), V);
-        const int at = slot * NC + c, qi = q - q_lo;
+        widen<BF16>(raw, x, row, whole(c), V);
+        const int at = slot * NC + c;
         const bool more = tn < t1;
         const int qn = more ? uni(tn / NC) : -1, cn = tn - qn * NC;
         if (more) {
@@ -269,74 +232,51 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
                 slot = uni(s_id[qn - q_lo]);
                 row = row_of(slot);
             }
-            issue_chunk<BF16>(raw, row, cn * kCH, whole(cn));
+            issue_chunk<BF16>(raw, row, cn * kCH, whole(cn), V);
         }
-        float vm[kVPL];
+        float lm = x[0][0];
 #pragma unroll
         for (int kk = 0; kk < kVPL; ++kk) {
-            float a = x[kk][0];
 #pragma unroll
-            for (int e = 1; e < E; ++e) a = fmaxf(a, x[kk][e]);
-            vm[kk] = a;
+            for (int e = 0; e < E; ++e) lm = fmaxf(lm, x[kk][e]);
         }
-        float lm = vm[0];
-#pragma unroll
-        for (int kk = 1; kk < kVPL; ++kk) lm = fmaxf(lm, vm[kk]);
         const float m = red_max_bc(lm);
-
-        int listed = 0;
         if (TOP) {
-            // elements equal to another wave's k-th best may still win by their column
-            const int shared = __atomic_load_n(&s_cut[qi], __ATOMIC_RELAXED);
-            int floor = max(best.cut, uni(shared) == kNoKey ? kNoKey : uni(shared) - 1);
-            const int lk = order_key(lm);
-            if (__ballot(lk > floor) != 0) {
-                if (floor == kNoKey) floor = kth_floor(lk, k);
-                offer<E>(best, floor, x, vm, vb, V, k);
-                if (best.cut > uni(shared) && lane == 0) atomicMax(&s_cut[qi], best.cut);
-            }
-            if (qn != q) {                     // the wave's last chunk of this slot: its list leaves
-                listed = __popcll(__ballot(best.key != kNoKey && lane < k));
-                if (lane < listed) P.cand[(int64_t)at * k + lane] = make_int2(best.key, best.col);
-                best = {kNoKey, 0, kNoKey};
-            }
+            char *to = P.lane_max + (int64_t)at * (64 * (16 / E));
+            if (BF16) ((uint16_t *)to)[lane] = (uint16_t)(__float_as_uint(lm) >> 16);
+            else ((float *)to)[lane] = lm;
         }
 
-        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, w4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        float s = 0.0f, w = 0.0f;
-        if (fabsf(m) <= kNearMax) {
-            const float nml = -m * kLog2e;
+        float near = m;                        // what the FMA takes off
+        if (!(fabsf(m) <= kNearMax)) {         // far from 0, or no finite logit: subtract first
+            near = 0.0f;
+            if (m != -INFINITY) {
 #pragma unroll
-            for (int kk = 0; kk < kVPL; ++kk) {
+                for (int kk = 0; kk < kVPL; ++kk) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float y = fmaf(x[kk][e], kLog2e, nml);
-                    const float p = __builtin_amdgcn_exp2f(y);
-                    s4[e % 4] += p;
-                    if (ENT) w4[e % 4] = fmaf(p, fmaxf(y, kFarBelow), w4[e % 4]);
+                    for (int e = 0; e < E; ++e) x[kk][e] -= m;
                 }
             }
-            const float r = fmaf(m, kLog2e, nml);          // what rounding nml added to every y
-            const float back = __builtin_amdgcn_exp2f(-r);
-            const float s1 = red_sum_bc((s4[0] + s4[1]) + (s4[2] + s4[3]));
-            s = s1 * back;
-            if (ENT) w = fmaf(-r, s1, red_sum_bc((w4[0] + w4[1]) + (w4[2] + w4[3]))) * back;
-        } else if (m != -INFINITY) {
-#pragma unroll
-            for (int kk = 0; kk < kVPL; ++kk) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float y = (x[kk][e] - m) * kLog2e;
-                    const float p = __builtin_amdgcn_exp2f(y);
-                    s4[e % 4] += p;
-                    if (ENT) w4[e % 4] = fmaf(p, fmaxf(y, kFarBelow), w4[e % 4]);
-                }
-            }
-            s = red_sum_bc((s4[0] + s4[1]) + (s4[2] + s4[3]));
-            if (ENT) w = red_sum_bc((w4[0] + w4[1]) + (w4[2] + w4[3]));
         }
+        const float nml = -near * kLog2e;
+        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, w4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kk = 0; kk < kVPL; ++kk) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float y = fmaf(x[kk][e], kLog2e, nml);
+                const float p = __builtin_amdgcn_exp2f(y);
+                s4[e % 4] += p;
+                if (ENT) w4[e % 4] = fmaf(p, fmaxf(y, kFarBelow), w4[e % 4]);
+            }
+        }
+        const float r = fmaf(near, kLog2e, nml);           // what rounding nml added to every y
+        const float back = __builtin_amdgcn_exp2f(-r);
+        const float s1 = red_sum_bc((s4[0] + s4[1]) + (s4[2] + s4[3]));
+        const float s = s1 * back;
+        const float w = ENT ? fmaf(-r, s1, red_sum_bc((w4[0] + w4[1]) + (w4[2] + w4[3]))) * back : 0.0f;
         if (lane == npend) {
-            pend = make_float4(m, s, w, __int_as_float(listed));
+            pend = make_float4(m, s, w, 0.0f);
             pend_at = at;
         }
         if (++npend == 64 || !more) {
@@ -349,32 +289,21 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
     }
 }
 
-// Kernel 2: one wave per selected slot.
+// Kernel 2, without alternatives: one wave per slot.
 constexpr int kJoinWaves = 4;
 
-template <bool BF16>
-__global__ __launch_bounds__(64 * kJoinWaves) void logprob_join_kernel(LogprobParams P) {
-    const int lane = lane_id();
-    const int slot = uni(blockIdx.x * kJoinWaves + (threadIdx.x >> 6));
-    if (slot >= P.rows * P.L) return;
-    fetch_args(P.mask, P.exclude, P.partials, P.tokens, P.token_stride, P.logits, P.NC, P.k);
-    if (P.mask[slot] == 0 || (P.exclude != nullptr && P.exclude[slot] != 0)) return;
-    const int r = slot / P.L, j = slot - r * P.L, NC = P.NC, k = P.k;
-    // the given token's logit, in flight beside the records
-    int tok = -1;
-    float xt = 0.0f;
-    if (P.tokens != nullptr) {
-        tok = P.tokens[(int64_t)r * P.token_stride + j];
-        if (tok >= 0 && tok < P.V) {
-            const char *row = P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
-            xt = BF16 ? __uint_as_float((uint32_t)((const uint16_t *)row)[tok] << 16) : ((const float *)row)[tok];
-        }
-    }
-    const float4 *rec = P.partials + (int64_t)slot * NC;
-    // each lane its records in order, then the lanes by a fixed tree
+struct Softmax {
+    float m, ls;                               // max, log sum
+    float h;                                   // entropy
+};
+
+// One wave: a slot's chunk records, each lane its own in order (the first one, record lane_id(), already
+// loaded), then the lanes by a fixed tree.  A row without a finite logit has a sum of 0: its log is
+// -inf, and -inf - -inf is the NaN reported.
+__device__ __forceinline__ Softmax join_records(const float4 *rec, int NC, float4 p) {
     float m = -INFINITY, s = 0.0f, w = 0.0f;
-    for (int c = lane; c < NC; c += 64) {
-        const float4 p = rec[c];
+    for (int c = lane_id(); c < NC; c += 64) {
+        if (c >= 64) p = rec[c];
         const float mm = fmaxf(m, p.x);
         if (mm == -INFINITY) continue;
         const float da = fmaxf((m - mm) * kLog2e, kFarBelow), db = fmaxf((p.x - mm) * kLog2e, kFarBelow);
@@ -388,51 +317,239 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprob_join_kernel(LogprobPa
     const float sc = __builtin_amdgcn_exp2f(d);
     w = red_sum_bc(sc * fmaf(d, s, w));
     s = red_sum_bc(sc * s);
-    // a row without a finite logit has s = 0: log s = -inf, and -inf - -inf is the NaN reported
     const float ls = logf(s);
-    if (lane == 0) {
-        if (P.logprob != nullptr) {
-            const bool ok = tok >= 0 && tok < P.V;
-            if (!ok) {
-                set_status(P.status, DLLM_ERR_ARG);
-                ((uint32_t *)P.logprob)[slot] = 0x7FC00000u;
-            } else {
-                P.logprob[slot] = (xt - mw) - ls;
+    return {mw, ls, fmaf(-kLn2, w / s, ls)};
+}
+__device__ __forceinline__ const char *slot_row(const LogprobParams &P, int slot) {
+    const int r = slot / P.L, j = slot - r * P.L;
+    return P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
+}
+// The given token's column; -1 for none, or one out of range.
+__device__ __forceinline__ int given_token(const LogprobParams &P, int slot) {
+    if (P.tokens == nullptr) return -1;
+    const int r = slot / P.L, j = slot - r * P.L;
+    const int t = P.tokens[(int64_t)r * P.token_stride + j];
+    return t >= 0 && t < P.V ? t : -1;
+}
+template <bool BF16>
+__device__ __forceinline__ float logit_at(const char *row, int col) {
+    return BF16 ? __uint_as_float((uint32_t)((const uint16_t *)row)[col] << 16) : ((const float *)row)[col];
+}
+__device__ __forceinline__ bool selected(const LogprobParams &P, int slot) {
+    return P.mask[slot] != 0 && (P.exclude == nullptr || P.exclude[slot] == 0);
+}
+__device__ __forceinline__ void write_slot(const LogprobParams &P, int slot, const Softmax &f, int tok, float x) {
+    if (P.logprob != nullptr) {
+        if (tok < 0) {
+            set_status(P.status, DLLM_ERR_ARG);
+            ((uint32_t *)P.logprob)[slot] = 0x7FC00000u;
+        } else {
+            P.logprob[slot] = (x - f.m) - f.ls;
+        }
+    }
+    if (P.entropy != nullptr) P.entropy[slot] = f.h;
+    if (P.stats != nullptr) P.stats[slot] = make_float2(f.m, f.ls);
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(64 * kJoinWaves) void logprob_join_kernel(LogprobParams P) {
+    const int slot = uni(blockIdx.x * kJoinWaves + (threadIdx.x >> 6));
+    if (slot >= P.rows * P.L) return;
+    fetch_args(P.mask, P.exclude, P.partials, P.tokens, P.token_stride, P.logits, P.NC);
+    // all three loads go out together, for a slot that is not selected too
+    const float4 *rec = P.partials + (int64_t)slot * P.NC;
+    const float4 first = rec[min(lane_id(), P.NC - 1)];
+    const int tok = given_token(P, slot);
+    if (!selected(P, slot)) return;
+    const float x = tok >= 0 ? logit_at<BF16>(slot_row(P, slot), tok) : 0.0f;
+    const Softmax f = join_records(rec, P.NC, first);
+    if (lane_id() == 0) write_slot(P, slot, f, tok, x);
+}
+
+// Kernel 2, with alternatives: one workgroup per slot.
+constexpr int kTopThreads = 64 * kJoinWaves;
+constexpr int kTopChunks = 20;                 // chunks per wave whose maxima stay in registers
+constexpr int kTopShares = 256;                // lane shares, and elements, the quick way has room for
+
+template <bool BF16>
+__global__ __launch_bounds__(kTopThreads) void logprob_top_kernel(LogprobParams P) {
+    typedef typename Row<BF16>::vec vec;
+    constexpr int E = Fmt<BF16>::E;
+    __shared__ int s_group[kJoinWaves][64];
+    __shared__ int s_share[kTopShares];
+    __shared__ int2 s_elem[kTopShares];
+    __shared__ int s_n[2];                     // shares, elements
+    __shared__ float s_f[2];
+    const int tid = threadIdx.x, lane = lane_id(), wave = uni(tid >> 6);
+    const int slot = blockIdx.x, NC = P.NC, V = P.V, k = P.k;
+    fetch_args(P.mask, P.exclude, P.partials, P.lane_max, P.tokens, P.token_stride, P.logits, P.NC, P.V, P.k);
+    const int tok = given_token(P, slot);
+    if (!selected(P, slot)) return;
+    const char *row = slot_row(P, slot);
+    const float4 *rec = P.partials + (int64_t)slot * NC;
+    // the last wave also joins the records: its loads go out now, their use waits for a quiet moment
+    const bool joins = wave == kJoinWaves - 1;
+    float4 first = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float xt = 0.0f;
+    if (joins) {
+        first = rec[min(lane, NC - 1)];
+        if (tok >= 0) xt = logit_at<BF16>(row, tok);
+    }
+    if (tid < 2) s_n[tid] = 0;
+
+    // Wave w holds chunks w, w + 4, ...: keys of this lane's maxima.  Lane l's maxima form group l; the
+    // k-th largest of the 64 group maxima is a lower bound of the k-th largest element.
+    int key[kTopChunks];
+    auto load_keys = [&](int c0) {
+        const char *lm = P.lane_max + ((int64_t)slot * NC) * (64 * (16 / E));
+#pragma unroll
+        for (int i = 0; i < kTopChunks; ++i) {
+            const int c = c0 + i * kJoinWaves + wave;
+            key[i] = kNoKey;
+            if (c < NC) {
+                const int64_t at = (int64_t)c * 64 + lane;
+                key[i] = BF16 ? (int)((const uint16_t *)lm)[at] << 16 : ((const int *)lm)[at];
             }
         }
-        if (P.entropy != nullptr) P.entropy[slot] = fmaf(-kLn2, w / s, ls);
-        if (P.stats != nullptr) P.stats[slot] = make_float2(mw, ls);
+#pragma unroll
+        for (int i = 0; i < kTopChunks; ++i)
+            if (c0 + i * kJoinWaves + wave < NC) key[i] = order_key(__int_as_float(key[i]));
+    };
+    constexpr int kSpan = kTopChunks * kJoinWaves;
+    int group = kNoKey;
+    for (int c0 = 0; c0 < NC; c0 += kSpan) {
+        load_keys(c0);
+#pragma unroll
+        for (int i = 0; i < kTopChunks; ++i) group = max(group, key[i]);
     }
-    if (k == 0) return;
+    s_group[wave][lane] = group;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWaves; ++w) group = max(group, s_group[w][lane]);
+    const int floor = kth_floor(group, k);
 
-    // candidate lists: 64 / k of them side by side, their entries in lane order.  A wave's list may
-    // span chunks that interleave with another's, so equals are ordered by column here.
-    const int2 *cand = P.cand + (int64_t)slot * NC * k;
-    Best b = {kNoKey, 0x7FFFFFFF, kNoKey};
-    const int side = 64 / k;
-    const int li = lane / k, le = lane - li * k;
-    for (int c0 = 0; c0 < NC; c0 += side) {
-        const int c = c0 + li;
-        int key = kNoKey, col = 0;
-        if (li < side && c < NC && le < __float_as_int(rec[c].w)) {
-            const int2 e = cand[(int64_t)c * k + le];
-            key = e.x;
-            col = e.y;
+    // Room for `mine` entries of this thread in a shared list: one atomic per wave.
+    auto room = [&](int mine, int *count) {
+        const int incl = wave_incl_scan(mine);
+        int at = 0;
+        if (lane == 63) at = incl > 0 ? atomicAdd(count, incl) : 0;
+        return __builtin_amdgcn_readlane(at, 63) + incl - mine;
+    };
+    // The lane shares (chunk, lane) above the bound.
+    for (int c0 = 0; c0 < NC; c0 += kSpan) {
+        if (NC > kSpan) load_keys(c0);
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < kTopChunks; ++i) mine += key[i] > floor;
+        int at = room(mine, &s_n[0]);
+        if (__ballot(mine > 0) != 0) {
+#pragma unroll
+            for (int i = 0; i < kTopChunks; ++i) {
+                if (key[i] > floor) {
+                    if (at < kTopShares) s_share[at] = (c0 + i * kJoinWaves + wave) * 64 + lane;
+                    ++at;
+                }
+            }
         }
-        int cut_col = __builtin_amdgcn_readlane(b.col, k - 1);
-        uint64_t in = __ballot(key != kNoKey && (key > b.cut || (key == b.cut && col < cut_col)));
-        while (in != 0) {
-            const int l = __builtin_ctzll(in);
-            const int nk = __builtin_amdgcn_readlane(key, l), nc = __builtin_amdgcn_readlane(col, l);
-            insert_at(b, __popcll(__ballot(b.key > nk || (b.key == nk && b.col < nc))), nk, nc, k);
-            cut_col = __builtin_amdgcn_readlane(b.col, k - 1);
-            in &= in - 1;
-            in &= __ballot(key > b.cut || (key == b.cut && col < cut_col));
+    }
+    __syncthreads();
+    const int shares = s_n[0];
+    auto load_share = [&](int share, int kk, float (&x)[E], int &col) {
+        const int v = (share >> 6) * kCH + kk * 64 + (share & 63);
+        col = v * E;
+        if (col + E <= V) {
+            const u32x4 raw = ((const vec *)row)[v];
+            unpack<BF16>(raw, x);
+        } else {
+            load_vec_elems<BF16>(row, min(v, P.NV), V, x);
+        }
+    };
+    // Their elements above the bound: at least k, with few more unless many logits are equal.
+    if (shares <= kTopShares) {
+        for (int i0 = wave * 64; i0 < shares * kVPL; i0 += kTopThreads) {
+            const int i = i0 + lane;
+            float x[E];
+            int col = V, mine = 0;
+            if (i < shares * kVPL) load_share(s_share[i / kVPL], i % kVPL, x, col);
+            int ek[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                ek[e] = col + e < V ? order_key(x[e]) : kNoKey;
+                mine += ek[e] > floor;
+            }
+            int at = room(mine, &s_n[1]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (ek[e] > floor) {
+                    if (at < kTopShares) s_elem[at] = make_int2(ek[e], col + e);
+                    ++at;
+                }
+            }
+        }
+    }
+    if (joins) {
+        const Softmax f = join_records(rec, NC, first);
+        if (lane == 0) {
+            write_slot(P, slot, f, tok, xt);
+            s_f[0] = f.m;
+            s_f[1] = f.ls;
+        }
+    }
+    __syncthreads();
+    const int elems = s_n[1];
+    const float m = s_f[0], ls = s_f[1];
+    if (shares <= kTopShares && elems <= kTopShares) {
+    // an element's place is the number of elements before it in the full order
+        if (tid < elems) {
+            const int2 own = s_elem[tid];
+            int place = 0;
+#pragma unroll 4
+            for (int i = 0; i < elems; ++i) {
+                const int2 o = s_elem[i];
+                place += o.x > own.x || (o.x == own.x && o.y < own.y);
+            }
+            if (place < k) {
+                P.top_ids[(int64_t)slot * k + place] = own.y;
+                P.top_lp[(int64_t)slot * k + place] = (key_value(own.x) - m) - ls;
+            }
+        }
+        return;
+    }
+    // Many logits equal to the k-th: wave 0 inserts share after share into a list sorted across its
+    // lanes.  Columns of a chunk lie above every column of the chunks before it, so once the list is
+    // full a share has to exceed its last entry, and the first chunks settle it.
+    if (wave != 0) return;
+    Best b = {kNoKey, 0x7FFFFFFF, kNoKey};
+    int cut_col = 0x7FFFFFFF;
+    const char *lm = P.lane_max + ((int64_t)slot * NC) * (64 * (16 / E));
+    for (int c = 0; c < NC; ++c) {
+        const int64_t at = (int64_t)c * 64 + lane;
+        const int ck = order_key(BF16 ? __uint_as_float((uint32_t)((const uint16_t *)lm)[at] << 16) : ((const float *)lm)[at]);
+        const bool on = ck > max(floor, b.cut);
+        if (__ballot(on) == 0) continue;
+#pragma unroll 1
+        for (int kk = 0; kk < kVPL; ++kk) {
+            float x[E];
+            int col = V;
+            if (on) load_share(c * 64 + lane, kk, x, col);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int ek = col + e < V ? order_key(x[e]) : kNoKey;
+                uint64_t in = __ballot(ek > floor && (ek > b.cut || (ek == b.cut && col + e < cut_col)));
+                while (in != 0) {
+                    const int l = __builtin_ctzll(in);
+                    const int nk = __builtin_amdgcn_readlane(ek, l), nc = __builtin_amdgcn_readlane(col + e, l);
+                    insert_at(b, __popcll(__ballot(b.key > nk || (b.key == nk && b.col < nc))), nk, nc, k);
+                    cut_col = __builtin_amdgcn_readlane(b.col, k - 1);
+                    in &= in - 1;
+                    in &= __ballot(ek > b.cut || (ek == b.cut && col + e < cut_col));
+                }
+            }
         }
     }
     if (lane < k) {
         P.top_ids[(int64_t)slot * k + lane] = b.col;
-        P.top_lp[(int64_t)slot * k + lane] = (key_value(b.key) - mw) - ls;
+        P.top_lp[(int64_t)slot * k + lane] = (key_value(b.key) - m) - ls;
     }
 }
 
@@ -550,12 +667,12 @@ __global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(GradParams P
 }
 
 // ---- host -----------------------------------------------------------------------------------------
-// Records and candidate lists of a workspace, each part 256-byte aligned.
+// Records and lane maxima (with alternatives only) of a workspace, each part 256-byte aligned.
 bool workspace_of(int32_t rows, int32_t L, int32_t V, int32_t k, int32_t dtype, int &NV, int &NC, size_t &records,
                   size_t &total) {
     if (k < 0 || k > DLLM_MAX_TOP || !shape_of(rows, L, V, dtype, NV, NC, records)) return false;
-    const size_t lists = ((size_t)rows * (size_t)L * (size_t)NC * (size_t)k * sizeof(int2) + 255) & ~(size_t)255;
-    total = records + lists;
+    const size_t maxima = (size_t)rows * (size_t)L * (size_t)NC * 64 * (dtype == DLLM_BF16 ? 2 : 4);
+    total = records + (k > 0 ? (maxima + 255) & ~(size_t)255 : 0);
     return true;
 }
 
@@ -624,7 +741,7 @@ extern "C" dllm_status dllm_logprobs(void *stream, const void *logits, int32_t d
     P.logprob = logprob; P.entropy = entropy; P.stats = (float2 *)stats;
     P.top_ids = top_ids; P.top_lp = top_logprobs;
     P.partials = (float4 *)workspace;
-    P.cand = (int2 *)((char *)workspace + records);
+    P.lane_max = (char *)workspace + records;
     P.status = status;
 
     // The scoring kernel's grid rule: the same chunks per workgroup, the same measured thresholds.
@@ -636,9 +753,9 @@ extern "C" dllm_status dllm_logprobs(void *stream, const void *logits, int32_t d
     grid = grid > most ? most : grid;
     const int64_t per = (boxed + grid - 1) / grid;
     const int win = (int)((per + P.NC - 1) / P.NC + 2);
-    const size_t lds = (size_t)win * sizeof(int) * (k > 0 ? 2 : 1);
+    const size_t lds = (size_t)win * sizeof(int);
     const bool bf = dtype == DLLM_BF16, ent = entropy != nullptr;
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, st, P, win); };
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, st, P); };
     if (bf) {
         if (k > 0) ent ? go(logprob_chunks_kernel<true, true, true>) : go(logprob_chunks_kernel<true, false, true>);
         else ent ? go(logprob_chunks_kernel<true, true, false>) : go(logprob_chunks_kernel<true, false, false>);
@@ -648,6 +765,11 @@ extern "C" dllm_status dllm_logprobs(void *stream, const void *logits, int32_t d
     }
     rc = check_hip(hipGetLastError(), "dllm_logprobs chunks launch");
     if (rc != DLLM_OK) return rc;
+    if (k > 0) {
+        if (bf) hipLaunchKernelGGL(logprob_top_kernel<true>, dim3((unsigned)S), dim3(kTopThreads), 0, st, P);
+        else hipLaunchKernelGGL(logprob_top_kernel<false>, dim3((unsigned)S), dim3(kTopThreads), 0, st, P);
+        return check_hip(hipGetLastError(), "dllm_logprobs alternatives launch");
+    }
     const dim3 jg((unsigned)((S + kJoinWaves - 1) / kJoinWaves)), jb(64 * kJoinWaves);
     if (bf) hipLaunchKernelGGL(logprob_join_kernel<true>, jg, jb, 0, st, P);
     else hipLaunchKernelGGL(logprob_join_kernel<false>, jg, jb, 0, st, P);

@@ -11,9 +11,9 @@ ARG, SHAPE, DTYPE = _lib.DLLM_ERR_ARG, _lib.DLLM_ERR_SHAPE, _lib.DLLM_ERR_DTYPE
 
 def test_workspace_sizes():
     L = _lib.lib()
-    # V = 152064 bf16: 38 chunks per slot; a record of 16 bytes and k candidates of 8 each
+    # V = 152064 bf16: 38 chunks per slot; a record of 16 bytes and 64 lane maxima of 2
     assert L.dllm_logprobs_workspace_bytes(64, 32, 152064, 0, 1) == 64 * 32 * 38 * 16
-    assert L.dllm_logprobs_workspace_bytes(64, 32, 152064, 20, 1) == 64 * 32 * 38 * (16 + 160)
+    assert L.dllm_logprobs_workspace_bytes(64, 32, 152064, 20, 1) == 64 * 32 * 38 * (16 + 128)
     assert L.dllm_logprobs_workspace_bytes(1, 1, 1, 1, 0) >= 24
     for bad in ((-1, 32, 100, 0, 1), (1, 0, 100, 0, 1), (1, 1, 0, 0, 1), (1, 1, 100, 33, 1), (1, 1, 100, -1, 1),
                 (1, 1, 100, 0, 2)):
@@ -37,7 +37,7 @@ def logprobs(**kw):
     (dict(logits=ctypes.c_void_p(0x100000001)), ARG), (dict(logits=ctypes.c_void_p(0x100000002), dtype=0), ARG),
     (dict(k=-1), ARG), (dict(k=33), ARG), (dict(k=5, V=4), ARG), (dict(tokens=None), ARG), (dict(lp=None), ARG),
     (dict(ti=None), ARG), (dict(tl=None), ARG), (dict(tokens=None, lp=None, ent=None, stats=None, k=0), ARG),
-    (dict(stats=ctypes.c_void_p(0x100000004)), ARG), (dict(ws=None), ARG), (dict(n=4 * 32 * 56 - 1), ARG),
+    (dict(stats=ctypes.c_void_p(0x100000004)), ARG), (dict(ws=None), ARG), (dict(n=4 * 32 * (16 + 128) - 1), ARG),
     (dict(ws=ctypes.c_void_p(0x100000008)), ARG),
     (dict(V=2 ** 31 - 1, ps=2 ** 31, rs=2 ** 36, rows=4096, L=32), SHAPE),
 ])
