@@ -28,4 +28,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
+// Lane i reads lane i-1; lane 0 keeps its own.  Every lane must be active.
+__device__ __forceinline__ int up_one(int v) { return wave_dpp::mov<0x138>(v, v); }
+
 }  // namespace dllm

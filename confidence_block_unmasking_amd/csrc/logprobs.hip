@@ -114,7 +114,6 @@ struct Best {
     int key, col;                              // this lane's entry
     int cut;                                   // key of entry k-1: what an element has to beat
 };
-__device__ __forceinline__ int up_one(int v) { return wave_dpp::mov<0x138>(v, v); }   // lane i reads lane i-1
 
 // Insert after `at` entries: the entries from there move up a lane.
 __device__ __forceinline__ void insert_at(Best &b, int at, int key, int col, int k) {
