@@ -6,9 +6,9 @@
 //
 //   out[n] = scale * table[ids[n]];     grad_table[v] (+)= scale * sum over tokens n of v of grad_out[n].
 //
-// Lookup (gfx950): a gather bound by HBM writes (and reads of the distinct rows).  The lanes of a
-// workgroup lie along the width, 8 elements each; the ids of kTokens tokens per thread load first,
-// then all their rows, then all stores.
+// Lookup (gfx950): a gather bound by HBM writes (and reads of the distinct rows).  A wave takes one token
+// and 2048 of its columns (kLookVecs vectors of 8 elements per lane, all in flight together); narrow
+// tables put several tokens side by side in a wave.
 //
 // Gradient: the tokens are sorted by id (stable, so a row's terms are summed in token order and the
 // bits never depend on timing; no float atomics), then every run of equal ids is summed once and
@@ -16,16 +16,18 @@
 //   1. Sort: least-significant-digit radix sort of (id, position), kDigit bits a pass, as few passes as
 //      the vocabulary's bits need.  A pass counts digits per tile, then moves the items; a wave finds
 //      an item's rank among equal digits by one ballot per digit bit.  One tile: all passes in one
-//      launch.  The sort keeps few compute units busy for some microseconds a launch, so each of its
-//      launches also writes zeros to a share of the table (kFillBytes).
+//      launch.  The sort keeps few compute units busy, so each of its launches also writes zeros to a
+//      share of the table, which hides the sort entirely behind a large table; rows that do occur
+//      are written again in step 2.  (Looking up which rows occur and clearing the others beside
+//      the sums instead took 317 us for 1.25 GB of bf16 table and 64 x 544 tokens; this takes 282.)
 //   2. Sum: one wave per piece of kPiece sorted tokens and 512 columns.  It loads kAhead tokens at a time
 //      whatever run they belong to (most runs are a token or two), adds them in order, and writes a
 //      row where a run ends.  A piece sums the runs that start in it, following the last one past its
 //      end, so runs up to kPiece tokens are never split.  A longer run (the mask token of a training
-//      box can hold half of all tokens) leaves one partial sum per piece it covers.  Other workgroups of
-//      the same launch write the remaining zeros, of ids that do not occur.
+//      box can hold half of all tokens) leaves one partial sum per piece it covers.
 //   3. Join: the partial sums of each long run, in order.
 #include <algorithm>
+#include <type_traits>
 
 #include "elem_common.h"
 
@@ -33,9 +35,9 @@ namespace {
 
 using namespace dllm;
 
-constexpr int kVec = 8;                        // elements per thread
-constexpr int kEmbedThreads = 256;
-constexpr int kTokens = 4;                     // tokens per thread, their loads in flight together
+constexpr int kVec = 8;                        // elements per vector
+constexpr int kLookWaves = 2;                  // waves per workgroup of the lookup
+constexpr int kLookVecs = 4;                   // vectors per lane
 
 // Elements [v*8, v*8 + 8) of a row of D: as stored, to keep several in flight, and widened.  Only a row's
 // ragged end is read element by element.
@@ -108,71 +110,87 @@ struct EmbedParams {
     int64_t out_stride_b;
     const int32_t *ids;
     const uint8_t *valid;
-    int32_t n, n_vocab, D, lanes_log2;         // a token's lanes: a power of two
+    int32_t n, n_vocab, D, nv;                 // nv: vectors of a row
+    int32_t lanes_log2, segs;                  // lanes per token (a power of two); waves per token when that is 64
     float scale;
     int32_t *status;
 };
 
-template <bool TB, bool OB>
-__global__ __launch_bounds__(kEmbedThreads) void embed_kernel(EmbedParams P) {
-    fetch_args(P.table, P.table_stride_b, P.out, P.out_stride_b, P.ids, P.valid, P.n, P.n_vocab, P.D, P.scale);
-    const int sub = threadIdx.x >> P.lanes_log2, lv = threadIdx.x & ((1 << P.lanes_log2) - 1);
-    const int per = kEmbedThreads >> P.lanes_log2;
-    const int nv = (P.D + kVec - 1) / kVec;
-    int id[kTokens];                           // the row to read, -1 for zeros
-    int tok[kTokens];
-#pragma unroll
-    for (int u = 0; u < kTokens; ++u) {
-        const int64_t t = ((int64_t)blockIdx.x * kTokens + u) * per + sub;
-        tok[u] = t < P.n ? (int)t : -1;
-        id[u] = -1;
-        if (tok[u] >= 0) {
-            id[u] = P.ids[t];
-            if (P.valid != nullptr && P.valid[t] == 0) id[u] = -1;
-            else if (id[u] < 0 || id[u] >= P.n_vocab) {
-                id[u] = -1;
-                if (lv == 0) set_status(P.status, DLLM_ERR_ARG);
-            }
-        }
+// WIDE: a whole wave per token, so the token and its id are wave-uniform (scalar loads).
+template <bool TB, bool OB, bool WIDE>
+__global__ __launch_bounds__(64 * kLookWaves) void embed_kernel(EmbedParams P) {
+    fetch_args(P.table, P.table_stride_b, P.out, P.out_stride_b, P.ids, P.valid, P.n, P.n_vocab, P.D, P.nv, P.scale);
+    const uint32_t unit = blockIdx.x * kLookWaves + uni(threadIdx.x >> 6);
+    const int lane = lane_id(), step = WIDE ? 64 : 1 << P.lanes_log2;
+    uint32_t t;
+    int v0;
+    if (WIDE) {
+        t = unit / P.segs;
+        v0 = (unit - t * P.segs) * (64 * kLookVecs) + lane;
+    } else {
+        t = (unit << (6 - P.lanes_log2)) + (lane >> P.lanes_log2);
+        v0 = lane & (step - 1);
     }
-    for (int v = lv; v < nv; v += 1 << P.lanes_log2) {
-        Raw<TB> raw[kTokens];
+    if (t >= (uint32_t)P.n) return;
+    int id = P.ids[t];                         // the row to read, -1 for zeros
+    if (P.valid != nullptr && P.valid[t] == 0) id = -1;
+    else if (id < 0 || id >= P.n_vocab) {
+        id = -1;
+        set_status(P.status, DLLM_ERR_ARG);
+    }
+    const char *row = P.table + id * P.table_stride_b;
+    char *out = P.out + t * P.out_stride_b;
+    Raw<TB> raw[kLookVecs];
 #pragma unroll
-        for (int u = 0; u < kTokens; ++u)
-            if (id[u] >= 0) raw[u] = load_raw<TB>(P.table + id[u] * P.table_stride_b, v, P.D);
+    for (int i = 0; i < kLookVecs; ++i) {
+        const int v = v0 + i * step;
+        if (id >= 0 && v < P.nv) raw[i] = load_raw<TB>(row, v, P.D);
+    }
 #pragma unroll
-        for (int u = 0; u < kTokens; ++u) {
-            if (tok[u] < 0) continue;
-            float x[kVec];
-            widen<TB>(raw[u], x);
+    for (int i = 0; i < kLookVecs; ++i) {
+        const int v = v0 + i * step;
+        if (v >= P.nv) continue;
+        float x[kVec];
+        widen<TB>(raw[i], x);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) x[e] = id[u] >= 0 ? x[e] * P.scale : 0.0f;
-            store8<OB>(P.out + tok[u] * P.out_stride_b, v, P.D, x);
-        }
+        for (int e = 0; e < kVec; ++e) x[e] = id >= 0 ? x[e] * P.scale : 0.0f;
+        store8<OB>(out, v, P.D, x);
     }
 }
 
 // ---- zeros ---------------------------------------------------------------------------------------
-constexpr int kFillRows = 64;                  // table rows a filling workgroup looks at
-// Bytes of zeros each launch of the sort writes beside it: what the card writes in about 6 us, as long
-// as such a launch takes.
-constexpr int64_t kFillBytes = 40 << 20;
-
 struct Table {
     char *p;
     int64_t stride_b;
-    int32_t n_vocab, D, lanes_log2;            // a row's lanes: a power of two
+    int32_t n_vocab, D, nv;                    // nv: 8-element vectors of a row
+    int32_t fill, fill_log2;                   // 16-byte vectors of a row (a ragged one too), also as a power of two not below it
 };
 
-// Rows v0 .. v0 + kFillRows - 1 whose bit is set in `rows`, by a workgroup of THREADS.
+// Rows a workgroup of `threads` clears: its threads lie along one row, or several narrow ones, one store
+// each for rows up to 16 bytes a thread.  One 16-byte store per thread in a dense sweep of the table writes
+// fastest: 6.3 TB/s over 1 GiB with 1024 threads, 5.6 with two stores, 5.5 with four.  Non-temporal, so the
+// zeros leave the last-level cache to the sums: 282 us for the whole gradient above, 312 with plain stores.
+constexpr int rows_at_once(int threads, int fill_log2) { return (1 << fill_log2) < threads ? threads >> fill_log2 : 1; }
+
 template <bool TB, int THREADS>
-__device__ __forceinline__ void fill_rows(const Table &T, int v0, uint64_t rows) {
-    const int nv = (T.D + kVec - 1) / kVec, lv = threadIdx.x & ((1 << T.lanes_log2) - 1);
-    const float z[kVec] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int r = threadIdx.x >> T.lanes_log2; r < kFillRows; r += THREADS >> T.lanes_log2) {
-        if (!((rows >> r) & 1)) continue;
-        char *row = T.p + (int64_t)(v0 + r) * T.stride_b;
-        for (int v = lv; v < nv; v += 1 << T.lanes_log2) store8<TB>(row, v, T.D, z);
+__device__ __forceinline__ void fill_rows(const Table &T, int first, int end) {
+    typedef typename Row<TB>::vec vec;
+    constexpr int E = TB ? 8 : 4;
+    const bool narrow = (1 << T.fill_log2) < THREADS;
+    const int v0 = narrow ? threadIdx.x & ((1 << T.fill_log2) - 1) : threadIdx.x;
+    const int r = first + (narrow ? threadIdx.x >> T.fill_log2 : 0);
+    if (r >= end) return;
+    char *row = T.p + r * T.stride_b;
+    const u32x4 z = {0, 0, 0, 0};
+    for (int v = v0; v < T.fill; v += THREADS) {
+        if ((v + 1) * E <= T.D) {
+            __builtin_nontemporal_store(z, (vec *)row + v);
+        } else {
+            for (int d = v * E; d < T.D; ++d) {
+                if (TB) ((uint16_t *)row)[d] = 0;
+                else ((float *)row)[d] = 0.0f;
+            }
+        }
     }
 }
 
@@ -218,8 +236,8 @@ __device__ __forceinline__ int digit_of(uint64_t item, int shift) { return (int)
 template <bool TB>
 __device__ __forceinline__ bool fills(const SortParams &P, int sorting) {
     if ((int)blockIdx.x < sorting) return false;
-    const int v0 = P.fill_first + ((int)blockIdx.x - sorting) * kFillRows, n = min(kFillRows, P.fill_end - v0);
-    fill_rows<TB, kSortThreads>(P.table, v0, n >= 64 ? ~0ull : (1ull << n) - 1);
+    const int first = P.fill_first + ((int)blockIdx.x - sorting) * rows_at_once(kSortThreads, P.table.fill_log2);
+    fill_rows<TB, kSortThreads>(P.table, first, P.fill_end);
     return true;
 }
 
@@ -248,19 +266,10 @@ __device__ __forceinline__ uint64_t same_digit(int d, bool on) {
     return m;
 }
 
-// Moves items [i0, i0 + tile) of one pass: `before` is the number of items of digit threadIdx.x in
-// earlier tiles, `total` in all tiles.  Wave w moves consecutive items, after those of waves < w.
-template <bool FIRST>
-__device__ __forceinline__ void move_tile(const SortParams &P, const uint64_t *in, uint64_t *out, int i0, int tile, int shift,
-                                          int before, int total, int (&s_at)[kSortWaves][kBins],
-                                          int (&s_wave)[kBins / 64]) {
+// Where each wave's next item of each digit goes, from the waves' counts in s_at: after the items of
+// smaller digits (`total` of digit threadIdx.x in all), those of earlier tiles (`before`) and waves.
+__device__ __forceinline__ void place_digits(int before, int total, int (&s_at)[kSortWaves][kBins], int (&s_wave)[kBins / 64]) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int b = tid; b < kSortWaves * kBins; b += kSortThreads) (&s_at[0][0])[b] = 0;
-    __syncthreads();
-    const int share = tile / kSortWaves, w0 = i0 + wave * share;
-    for (int i = w0 + lane; i < w0 + share; i += 64)
-        if (i < P.n) atomicAdd(&s_at[wave][digit_of(sort_item<FIRST>(P, in, i, false), shift)], 1);
-    // where each digit starts in the output: the totals of the digits below it
     int incl = 0;
     if (tid < kBins) {
         incl = wave_incl_scan(total);
@@ -270,6 +279,7 @@ __device__ __forceinline__ void move_tile(const SortParams &P, const uint64_t *i
     if (tid < kBins) {
         int at = incl - total + before;
         for (int w = 0; w < wave; ++w) at += s_wave[w];
+#pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
             const int c = s_at[w][tid];
             s_at[w][tid] = at;
@@ -277,32 +287,30 @@ __device__ __forceinline__ void move_tile(const SortParams &P, const uint64_t *i
         }
     }
     __syncthreads();
-    for (int i = w0 + lane; i - lane < w0 + share; i += 64) {
-        const bool on = i < P.n;
-        const uint64_t item = on ? sort_item<FIRST>(P, in, i, false) : 0;
-        const int d = digit_of(item, shift);
-        const uint64_t peers = same_digit(d, on);
-        const int rank = __popcll(peers & ((1ull << lane) - 1));
-        int at = 0;
-        if (on) {
-            at = __atomic_load_n(&s_at[wave][d], __ATOMIC_RELAXED);
-            out[at + rank] = item;
-        }
-        // every lane has read its digit's place before the first lane of that digit moves it on
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (on && rank == 0) __atomic_store_n(&s_at[wave][d], at + __popcll(peers), __ATOMIC_RELAXED);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    }
+}
+// The place of this lane's item, the wave's lanes in order; `at` is the wave's row of s_at.
+__device__ __forceinline__ int take_place(int *at, int d, bool on) {
+    const uint64_t peers = same_digit(d, on);
+    const int rank = __popcll(peers & ((1ull << lane_id()) - 1));
+    int first = 0;
+    if (on) first = __atomic_load_n(&at[d], __ATOMIC_RELAXED);
+    // every lane has read its digit's place before the first lane of that digit moves it on
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (on && rank == 0) __atomic_store_n(&at[d], first + __popcll(peers), __ATOMIC_RELAXED);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    return first + rank;
 }
 
+// Moves a tile's items; wave w moves consecutive ones, after those of waves < w.
 template <bool FIRST, bool TB>
 __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(SortParams P) {
     __shared__ int s_at[kSortWaves][kBins];
     __shared__ int s_wave[kBins / 64];
     if (fills<TB>(P, P.tiles)) return;
-    const int tid = threadIdx.x, mine = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, mine = blockIdx.x;
+    for (int b = tid; b < kSortWaves * kBins; b += kSortThreads) (&s_at[0][0])[b] = 0;
     int before = 0, total = 0;
     if (tid < kBins) {
 #pragma unroll 8
@@ -312,44 +320,81 @@ __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(SortParams P) {
             total += c;
         }
     }
-    move_tile<FIRST>(P, P.in, P.out, mine * P.tile, P.tile, P.shift, before, total, s_at, s_wave);
+    __syncthreads();
+    const int share = P.tile / kSortWaves, w0 = mine * P.tile + wave * share;
+    for (int i = w0 + lane; i < w0 + share; i += 64)
+        if (i < P.n) atomicAdd(&s_at[wave][digit_of(sort_item<FIRST>(P, P.in, i, false), P.shift)], 1);
+    __syncthreads();
+    place_digits(before, total, s_at, s_wave);
+    for (int i = w0 + lane; i - lane < w0 + share; i += 64) {
+        const bool on = i < P.n;
+        const uint64_t item = on ? sort_item<FIRST>(P, P.in, i, false) : 0;
+        const int at = take_place(s_at[wave], digit_of(item, P.shift), on);
+        if (on) P.out[at] = item;
+    }
 }
 
-// One tile: every pass in one workgroup.  The items go through global memory between the passes.
+// One tile: every pass in one workgroup, the items in LDS between the passes.
+constexpr int kHeld = kMinTile / kSortThreads;   // items per thread
+
 template <bool TB>
 __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(SortParams P) {
     __shared__ int s_at[kSortWaves][kBins];
     __shared__ int s_wave[kBins / 64];
-    __shared__ int s_count[kBins];
+    __shared__ uint64_t s_item[kMinTile];
     if (fills<TB>(P, 1)) return;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int share = P.tile / kSortWaves, w0 = wave * share;
     if (tid == 0) *P.n_long = 0;
-    const uint64_t *in = P.in;
-    uint64_t *out = P.out;
+    uint64_t item[kHeld];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        const int i = w0 + h * 64 + lane;
+        item[h] = 0;
+        if (h * 64 < share && i < P.n) item[h] = first_item(P, i, true);
+    }
     for (int shift = 0; shift < P.bits; shift += kDigit) {
-        if (tid < kBins) s_count[tid] = 0;
+        for (int b = tid; b < kSortWaves * kBins; b += kSortThreads) (&s_at[0][0])[b] = 0;
         __syncthreads();
-        for (int i = tid; i < P.n; i += kSortThreads) {
-            const uint64_t item = shift == 0 ? first_item(P, i, true) : in[i];
-            atomicAdd(&s_count[digit_of(item, shift)], 1);
+        if (shift > 0) {
+#pragma unroll
+            for (int h = 0; h < kHeld; ++h)
+                if (h * 64 < share) item[h] = s_item[w0 + h * 64 + lane];
+        }
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (h * 64 < share && w0 + h * 64 + lane < P.n) atomicAdd(&s_at[wave][digit_of(item[h], shift)], 1);
+        __syncthreads();
+        int total = 0;
+        if (tid < kBins) {
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) total += s_at[w][tid];
+        }
+        place_digits(0, total, s_at, s_wave);
+        const bool last = shift + kDigit >= P.bits;
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            if (h * 64 >= share) continue;
+            const bool on = w0 + h * 64 + lane < P.n;
+            const int at = take_place(s_at[wave], digit_of(item[h], shift), on);
+            if (on) {
+                if (last) P.out[at] = item[h];
+                else s_item[at] = item[h];
+            }
         }
         __syncthreads();
-        const int total = tid < kBins ? s_count[tid] : 0;
-        if (shift == 0) move_tile<true>(P, in, out, 0, P.tile, shift, 0, total, s_at, s_wave);
-        else move_tile<false>(P, in, out, 0, P.tile, shift, 0, total, s_at, s_wave);
-        __syncthreads();
-        uint64_t *t = (uint64_t *)in;
-        in = out;
-        out = t;
     }
 }
 
 // ---- sum and join ---------------------------------------------------------------------------------
-constexpr int kPiece = 64;
+// Sorted tokens per piece: many where there is work for every compute unit, few where a wave's own chain of
+// loads is what takes the time (see launch).
+constexpr int kPiece = 64, kSmallPiece = 16;
 constexpr int kSumThreads = 256;
 constexpr int kSumWaves = kSumThreads / 64;
 constexpr int kSumCols = 64 * kVec;            // columns per wave
-constexpr int kAhead = 8;                      // tokens whose loads are in flight together
+// Tokens whose loads are in flight together; with the table's old rows beside them, half as many.
+constexpr int kAhead = 8, kAheadOld = 4;
 
 struct SumParams {
     const char *grad;
@@ -358,7 +403,7 @@ struct SumParams {
     const uint64_t *sorted;
     float *part;                               // [pieces][2][D]: the run entering from before, the run leaving
     int32_t *n_long, *long_piece;              // pieces in which a long run starts
-    int32_t n, pieces, colblocks, accumulate, sum_blocks, fill_first;
+    int32_t n, pieces, colblocks, accumulate;
     float scale;
 };
 
@@ -366,105 +411,151 @@ __device__ __forceinline__ int key_of(uint64_t item) { return (int)(item >> 32);
 
 // table row = (old +) scale * sum, rounded once.
 template <bool TB>
-__device__ __forceinline__ void write_row(const SumParams &P, int id, int v, const float (&a)[kVec]) {
-    char *row = P.table.p + id * P.table.stride_b;
+__device__ __forceinline__ void write_row(const SumParams &P, int id, int v, const float (&a)[kVec], const float (&old)[kVec]) {
     float o[kVec];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) o[e] = 0.0f;
-    if (P.accumulate) widen<TB>(load_raw<TB>(row, v, P.table.D), o);
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) o[e] = fmaf(P.scale, a[e], o[e]);
-    store8<TB>(row, v, P.table.D, o);
+    for (int e = 0; e < kVec; ++e) o[e] = fmaf(P.scale, a[e], old[e]);
+    store8<TB>(P.table.p + id * P.table.stride_b, v, P.table.D, o);
 }
 
-// One wave: piece `piece`, columns colblock*512 ...  Positions in the window of three pieces around it:
-// [64, 128) is the piece itself.
-template <bool GB, bool TB>
+// The window of three pieces around piece [N, 2N): ids, positions and run starts, spread over the lanes.
+template <int N>
+struct Window;
+template <>
+struct Window<64> {
+    int k0, k1, k2, p1, p2;
+    __device__ __forceinline__ void load(const uint64_t *sorted, int64_t first, int n, uint64_t none) {
+        const int64_t i = first + lane_id();
+        const uint64_t w0 = i >= 64 ? sorted[i - 64] : none, w1 = i < n ? sorted[i] : none,
+                       w2 = i + 64 < n ? sorted[i + 64] : none;
+        k0 = (int)(w0 >> 32), k1 = (int)(w1 >> 32), k2 = (int)(w2 >> 32), p1 = (int)(uint32_t)w1, p2 = (int)(uint32_t)w2;
+    }
+    // bits of the positions whose id differs from the one before (the window's first position counts)
+    __device__ __forceinline__ void starts(uint64_t &s0, uint64_t &s1, uint64_t &s2) const {
+        const int lane = lane_id(), b0 = up_one(k0), b1 = up_one(k1), b2 = up_one(k2);
+        s0 = __ballot(lane == 0 || k0 != b0);
+        s1 = __ballot(k1 != (lane == 0 ? __builtin_amdgcn_readlane(k0, 63) : b1));
+        s2 = __ballot(k2 != (lane == 0 ? __builtin_amdgcn_readlane(k1, 63) : b2));
+    }
+    __device__ __forceinline__ void counts(int none, int &c1, int &c2) const {   // tokens with an id
+        c1 = __popcll(__ballot(k1 != none));
+        c2 = __popcll(__ballot(k2 != none));
+    }
+    __device__ __forceinline__ int key(int t) const {
+        return t < 128 ? __builtin_amdgcn_readlane(k1, t - 64) : __builtin_amdgcn_readlane(k2, t - 128);
+    }
+    __device__ __forceinline__ int pos(int t) const {
+        return t < 128 ? __builtin_amdgcn_readlane(p1, t - 64) : __builtin_amdgcn_readlane(p2, t - 128);
+    }
+};
+template <>
+struct Window<16> {
+    int k, p;                                  // lanes 0 .. 47
+    __device__ __forceinline__ void load(const uint64_t *sorted, int64_t first, int n, uint64_t none) {
+        const int64_t i = first - 16 + lane_id();
+        const uint64_t w = i >= 0 && i < n && lane_id() < 48 ? sorted[i] : none;
+        k = (int)(w >> 32), p = (int)(uint32_t)w;
+    }
+    __device__ __forceinline__ void starts(uint64_t &s0, uint64_t &s1, uint64_t &s2) const {
+        const int below = up_one(k);
+        const uint64_t s = __ballot(lane_id() == 0 || k != below);
+        s0 = s & 0xFFFF, s1 = (s >> 16) & 0xFFFF, s2 = (s >> 32) & 0xFFFF;
+    }
+    __device__ __forceinline__ void counts(int none, int &c1, int &c2) const {
+        const uint64_t on = __ballot(k != none);
+        c1 = __popcll((on >> 16) & 0xFFFF), c2 = __popcll((on >> 32) & 0xFFFF);
+    }
+    __device__ __forceinline__ int key(int t) const { return __builtin_amdgcn_readlane(k, t); }
+    __device__ __forceinline__ int pos(int t) const { return __builtin_amdgcn_readlane(p, t); }
+};
+
+// One wave: piece `piece`, columns colblock*512 ...
+template <bool GB, bool TB, int N, bool OLD>
 __device__ void sum_piece(const SumParams &P, int piece, int colblock) {
-    const int lane = lane_id(), D = P.table.D;
-    const int64_t i0 = (int64_t)piece * kPiece + lane;
-    const uint64_t none = (uint64_t)P.table.n_vocab << 32;         // a token that adds nothing
-    const uint64_t w0 = i0 >= kPiece ? P.sorted[i0 - kPiece] : none;
-    const uint64_t w1 = i0 < P.n ? P.sorted[i0] : none;
-    const uint64_t w2 = i0 + kPiece < P.n ? P.sorted[i0 + kPiece] : none;
-    const int k0 = key_of(w0), k1 = key_of(w1), k2 = key_of(w2), p1 = (int)(uint32_t)w1, p2 = (int)(uint32_t)w2;
-    // run starts as bits; ids stop at the first token that adds nothing
-    auto starts = [&](int k, int previous) {
-        const int below = up_one(k);           // before the choice: every lane takes part
-        return __ballot(k != (lane == 0 ? previous : below));
-    };
-    const uint64_t s0 = starts(k0, -1), s1 = starts(k1, __builtin_amdgcn_readlane(k0, 63)),
-                   s2 = starts(k2, __builtin_amdgcn_readlane(k1, 63));
-    const int ids1 = __popcll(__ballot(k1 != P.table.n_vocab)), ids2 = __popcll(__ballot(k2 != P.table.n_vocab));
-    if (ids1 == 0) return;
-    // first start at or after window position i >= 64 (192: none in the window)
+    constexpr int kStep = OLD ? kAheadOld : kAhead;
+    const int D = P.table.D, none = P.table.n_vocab;               // `none`: tokens that add nothing, last
+    Window<N> w;
+    w.load(P.sorted, (int64_t)piece * N, P.n, (uint64_t)none << 32);
+    uint64_t s0, s1, s2;
+    int c1, c2;
+    w.starts(s0, s1, s2);
+    w.counts(none, c1, c2);
+    if (c1 == 0) return;
+    // first start at or after window position i >= N (3N: none in the window)
     auto next_start = [&](int i) {
-        if (i < 128) {
-            const uint64_t m = s1 & (~0ull << (i - 64));
-            if (m != 0) return 64 + (int)__builtin_ctzll(m);
-            i = 128;
+        if (i < 2 * N) {
+            const uint64_t m = s1 & (~0ull << (i - N));
+            if (m != 0) return N + (int)__builtin_ctzll(m);
+            i = 2 * N;
         }
-        const uint64_t m = i < 192 ? s2 & (~0ull << (i - 128)) : 0ull;
-        return m != 0 ? 128 + (int)__builtin_ctzll(m) : 192;
+        const uint64_t m = i < 3 * N ? s2 & (~0ull << (i - 2 * N)) : 0ull;
+        return m != 0 ? 2 * N + (int)__builtin_ctzll(m) : 3 * N;
     };
-    int begin = 64, end;
+    int begin = N, end;
     // the run that enters from the piece before: its part here if it is long, nothing otherwise
-    int head_end = 0;                          // > 0: tokens [64, head_end) go to partial sum 0
+    int head_end = 0;                          // > 0: tokens [N, head_end) go to partial sum 0
     if (!(s1 & 1)) {
-        const int lo = s0 != 0 ? 63 - (int)__builtin_clzll(s0) : 0, hi = next_start(65);
-        if (hi - lo > kPiece) head_end = min(hi, 128);
+        const int lo = 63 - (int)__builtin_clzll(s0), hi = next_start(N + 1);
+        if (hi - lo > N) head_end = min(hi, 2 * N);
         else begin = hi;
     }
     // the last run that starts here: to its end, or to the piece's end and into partial sum 1 if it is long
-    int tail = 192;                            // < 192: where a long run starts
-    if (ids1 < 64) {
-        end = 64 + ids1;
+    int tail = 3 * N;                          // < 3N: where a long run starts
+    if (c1 < N) {
+        end = N + c1;
     } else if (s1 != 0) {
-        const int last = 127 - (int)__builtin_clzll(s1), hi = next_start(last + 1);
-        end = min(hi, 128 + ids2);
-        if (hi - last > kPiece) {
+        const int last = N + 63 - (int)__builtin_clzll(s1), hi = next_start(last + 1);
+        end = min(hi, 2 * N + c2);
+        if (hi - last > N) {
             tail = last;
-            end = 128;
+            end = 2 * N;
         }
     } else {
-        end = 128;                             // one run covers the piece: head_end is set, or nothing starts here
+        end = 2 * N;                           // one long run covers the piece
     }
     if (begin >= end) return;
-    if (tail < 192 && colblock == 0 && lane == 0) P.long_piece[atomicAdd(P.n_long, 1)] = piece;
+    if (tail < 3 * N && colblock == 0 && lane_id() == 0) P.long_piece[atomicAdd(P.n_long, 1)] = piece;
 
     // lanes past the last column keep running (their registers are read across the wave) on its vector
-    const int nv = (D + kVec - 1) / kVec, own = colblock * 64 + lane, v = min(own, nv - 1);
-    const bool live = own < nv;
+    const int own = colblock * 64 + lane_id(), v = min(own, P.table.nv - 1);
+    const bool live = own < P.table.nv;
+    auto ends_run = [&](int t) { return t + 1 == end || next_start(t + 1) == t + 1; };
+    auto to_row = [&](int t) { return t + 1 != head_end && t < tail; };
     float a[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) a[e] = 0.0f;
-    for (int t0 = begin; t0 < end; t0 += kAhead) {
-        Raw<GB> raw[kAhead];
+    for (int t0 = begin; t0 < end; t0 += kStep) {
+        Raw<GB> raw[kStep];
+        Raw<TB> old[kStep];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kStep; ++u) {
             const int t = t0 + u;
             if (t < end) {
-                const int pos = t < 128 ? __builtin_amdgcn_readlane(p1, t - 64) : __builtin_amdgcn_readlane(p2, t - 128);
-                raw[u] = load_raw<GB>(P.grad + pos * P.grad_stride_b, v, D);
+                raw[u] = load_raw<GB>(P.grad + w.pos(t) * P.grad_stride_b, v, D);
+                if (OLD && ends_run(t) && to_row(t)) old[u] = load_raw<TB>(P.table.p + w.key(t) * P.table.stride_b, v, D);
             }
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kStep; ++u) {
             const int t = t0 + u;
             if (t >= end) break;
             float x[kVec];
             widen<GB>(raw[u], x);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) a[e] += x[e];
-            if (t + 1 < end && next_start(t + 1) != t + 1) continue;
-            if (t + 1 == head_end || (t >= tail && t + 1 == end)) {
+            if (!ends_run(t)) continue;
+            if (to_row(t)) {
+                float o[kVec];
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) o[e] = 0.0f;
+                if (OLD) widen<TB>(old[u], o);
+                const int id = w.key(t);
+                if (live) write_row<TB>(P, id, v, a, o);
+            } else {
                 float *part = P.part + ((int64_t)piece * 2 + (t + 1 == head_end ? 0 : 1)) * D;
 #pragma unroll
                 for (int e = 0; e < kVec; ++e)
                     if (live && v * kVec + e < D) part[v * kVec + e] = a[e];
-            } else {
-                const int id = t < 128 ? __builtin_amdgcn_readlane(k1, t - 64) : __builtin_amdgcn_readlane(k2, t - 128);
-                if (live) write_row<TB>(P, id, v, a);
             }
 #pragma unroll
             for (int e = 0; e < kVec; ++e) a[e] = 0.0f;
@@ -472,39 +563,10 @@ __device__ void sum_piece(const SumParams &P, int piece, int colblock) {
     }
 }
 
-// First sorted position whose id is at least `key`.
-__device__ __forceinline__ int first_at_least(const uint64_t *sorted, int n, int key) {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (key_of(sorted[mid]) < key) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
-
-template <bool GB, bool TB>
+template <bool GB, bool TB, int N, bool OLD>
 __global__ __launch_bounds__(kSumThreads) void embed_sum_kernel(SumParams P) {
-    if ((int)blockIdx.x < P.sum_blocks) {
-        const int unit = (int)blockIdx.x * kSumWaves + uni(threadIdx.x >> 6);
-        if (unit < P.pieces * P.colblocks) sum_piece<GB, TB>(P, uni(unit / P.colblocks), uni(unit % P.colblocks));
-        return;
-    }
-    // zeros for ids without a token
-    __shared__ uint64_t s_absent;
-    const int v0 = P.fill_first + ((int)blockIdx.x - P.sum_blocks) * kFillRows, tid = threadIdx.x;
-    if (tid < kFillRows) {
-        const int id = v0 + tid;
-        bool absent = id < P.table.n_vocab;
-        if (absent) {
-            const int at = first_at_least(P.sorted, P.n, id);
-            absent = at >= P.n || key_of(P.sorted[at]) != id;
-        }
-        const uint64_t b = __ballot(absent);
-        if (tid == 0) s_absent = b;
-    }
-    __syncthreads();
-    fill_rows<TB, kSumThreads>(P.table, v0, s_absent);
+    const int unit = (int)blockIdx.x * kSumWaves + uni(threadIdx.x >> 6);
+    if (unit < P.pieces * P.colblocks) sum_piece<GB, TB, N, OLD>(P, uni(unit / P.colblocks), uni(unit % P.colblocks));
 }
 
 // The partial sums of each long run: 16 threads side by side on 4 columns each, 16 slices of pieces.
@@ -512,7 +574,7 @@ constexpr int kJoinCols = 64, kJoinSlices = 16;
 
 constexpr int kJoinRuns = 16;                  // long runs side by side
 
-template <bool TB>
+template <bool TB, int N>
 __global__ __launch_bounds__(256) void embed_join_kernel(SumParams P) {
     __shared__ float s_sum[kJoinSlices][kJoinCols];
     __shared__ int s_more[4];
@@ -521,11 +583,11 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams P) {
     const int n_long = *P.n_long;
     for (int l = blockIdx.y; l < n_long; l += gridDim.y) {
         const int p0 = P.long_piece[l];
-        const int key = key_of(P.sorted[(int64_t)p0 * kPiece + kPiece - 1]);
+        const int key = key_of(P.sorted[(int64_t)p0 * N + N - 1]);
         // the pieces after p0 that start with the run's id, 256 at a time
         int count = 1;
         while (true) {
-            const int64_t i = ((int64_t)p0 + count + tid) * kPiece;
+            const int64_t i = ((int64_t)p0 + count + tid) * N;
             const uint64_t in = __ballot(i < P.n && key_of(P.sorted[i]) == key);
             if ((tid & 63) == 0) s_more[tid >> 6] = __popcll(in);
             __syncthreads();
@@ -538,10 +600,16 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams P) {
         float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
         for (int p = slice * per; p < min((slice + 1) * per, count); ++p) {
-            const float *part = P.part + ((int64_t)(p0 + p) * 2 + (p == 0 ? 1 : 0)) * D;
+            const float *part = P.part + ((int64_t)(p0 + p) * 2 + (p == 0 ? 1 : 0)) * D + col;
+            if (col + 4 <= D) {
+                const u32x4 x = *(const Row<false>::vec *)part;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (col + e < D) a[e] += part[col + e];
+                for (int e = 0; e < 4; ++e) a[e] += __uint_as_float(x[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < D) a[e] += part[e];
+            }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) s_sum[slice][c + e] = a[e];
@@ -554,16 +622,24 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams P) {
                 t[e] = 0.0f;
                 for (int s = 0; s < kJoinSlices; ++s) t[e] += s_sum[s][tid * kVec + e];
             }
-            if (v * kVec < D) write_row<TB>(P, key, v, t);
+            if (v * kVec < D) {
+                float o[kVec];
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) o[e] = 0.0f;
+                if (P.accumulate) widen<TB>(load_raw<TB>(P.table.p + key * P.table.stride_b, v, D), o);
+                write_row<TB>(P, key, v, t, o);
+            }
         }
         __syncthreads();
     }
 }
 
 // ---- host -----------------------------------------------------------------------------------------
+constexpr int64_t kSmallUnits = 2048;
+
 struct GradSpace {
     size_t a, b, hist, n_long, long_piece, part, bytes;
-    int tile, tiles, pieces;
+    int tile, tiles, piece, pieces;
 };
 GradSpace grad_space(int64_t n, int64_t D) {
     GradSpace w{};
@@ -571,7 +647,11 @@ GradSpace grad_space(int64_t n, int64_t D) {
     if (w.tile == 0) w.tile = kSortThreads;
     while ((n + w.tile - 1) / w.tile > kMaxTiles) w.tile *= 2;
     w.tiles = (int)((n + w.tile - 1) / w.tile);
-    w.pieces = (int)((n + kPiece - 1) / kPiece);
+    // Fewer than kSmallUnits waves at kPiece tokens leave compute units idle while each wave works through
+    // its tokens: shorter pieces then.
+    const int64_t units = (n + kPiece - 1) / kPiece * ((D + kSumCols - 1) / kSumCols);
+    w.piece = units < kSmallUnits ? kSmallPiece : kPiece;
+    w.pieces = (int)((n + w.piece - 1) / w.piece);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -602,11 +682,11 @@ dllm_status check_sizes(const char *who, int32_t n_tokens, int32_t n_vocab, int3
         return fail(DLLM_ERR_ARG, "%s: strides %lld, %lld smaller than D=%d", who, (long long)stride_a, (long long)stride_b, D);
     return DLLM_OK;
 }
-// log2 of the lanes that share a row of D: as many as its 8-element vectors, in a workgroup of 256.
-int lanes_of(int32_t D) {
-    const int nv = (D + kVec - 1) / kVec;
+int vectors_of(int32_t D) { return (D + kVec - 1) / kVec; }
+// log2 of the smallest power of two not below n
+int log2_up(int n) {
     int l = 0;
-    while ((1 << l) < nv && (1 << l) < kEmbedThreads) ++l;
+    while ((1 << l) < n) ++l;
     return l;
 }
 bool misaligned(const void *p, int32_t dtype) { return ((uintptr_t)p & (dtype == DLLM_BF16 ? 1 : 3)) != 0; }
@@ -638,16 +718,22 @@ extern "C" dllm_status dllm_embed(void *stream, const void *table, int32_t table
     P.n = n_tokens; P.n_vocab = n_vocab; P.D = D;
     P.scale = scale;
     P.status = status;
-    P.lanes_log2 = lanes_of(D);
-    const int64_t per = (int64_t)(kEmbedThreads >> P.lanes_log2) * kTokens;
-    const dim3 grid((unsigned)((n_tokens + per - 1) / per)), block(kEmbedThreads);
+    P.nv = vectors_of(D);
+    P.lanes_log2 = std::min(log2_up(P.nv), 6);
+    P.segs = (P.nv + 64 * kLookVecs - 1) / (64 * kLookVecs);
+    const bool wide = P.lanes_log2 == 6;
+    const int per = 64 >> P.lanes_log2;
+    const int64_t units = wide ? (int64_t)n_tokens * P.segs : ((int64_t)n_tokens + per - 1) / per;
+    const int64_t blocks = (units + kLookWaves - 1) / kLookWaves;
+    if (blocks >= (int64_t)1 << 31) return fail(DLLM_ERR_SHAPE, "%s: n_tokens * D too large", who);
     const hipStream_t st = (hipStream_t)stream;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * kLookWaves), 0, st, P); };
     if (table_dtype == DLLM_BF16) {
-        if (out_dtype == DLLM_BF16) hipLaunchKernelGGL((embed_kernel<true, true>), grid, block, 0, st, P);
-        else hipLaunchKernelGGL((embed_kernel<true, false>), grid, block, 0, st, P);
+        if (out_dtype == DLLM_BF16) wide ? go(embed_kernel<true, true, true>) : go(embed_kernel<true, true, false>);
+        else wide ? go(embed_kernel<true, false, true>) : go(embed_kernel<true, false, false>);
     } else {
-        if (out_dtype == DLLM_BF16) hipLaunchKernelGGL((embed_kernel<false, true>), grid, block, 0, st, P);
-        else hipLaunchKernelGGL((embed_kernel<false, false>), grid, block, 0, st, P);
+        if (out_dtype == DLLM_BF16) wide ? go(embed_kernel<false, true, true>) : go(embed_kernel<false, true, false>);
+        else wide ? go(embed_kernel<false, false, true>) : go(embed_kernel<false, false, false>);
     }
     return check_hip(hipGetLastError(), "dllm_embed launch");
 }
@@ -676,17 +762,19 @@ extern "C" dllm_status dllm_embed_grad(void *stream, const void *grad_out, int32
         return fail(DLLM_ERR_ARG, "%s: workspace %zu bytes < %zu needed", who, workspace_bytes, w.bytes);
     if (((uintptr_t)workspace & 255) != 0) return fail(DLLM_ERR_ARG, "%s: workspace not 256-byte aligned", who);
     const size_t tbytes = ((size_t)(n_vocab - 1) * table_stride + D) * ts;
-    const size_t gb = n_tokens ? ((size_t)(n_tokens - 1) * grad_stride + D) * gs : 0;
-    if (overlap(grad_table, tbytes, grad_out, gb) || overlap(grad_table, tbytes, ids, (size_t)n_tokens * 4) ||
+    const size_t gbytes = n_tokens ? ((size_t)(n_tokens - 1) * grad_stride + D) * gs : 0;
+    if (overlap(grad_table, tbytes, grad_out, gbytes) || overlap(grad_table, tbytes, ids, (size_t)n_tokens * 4) ||
         (valid && overlap(grad_table, tbytes, valid, n_tokens)) || overlap(grad_table, tbytes, workspace, w.bytes) ||
-        overlap(workspace, w.bytes, grad_out, gb) || overlap(workspace, w.bytes, ids, (size_t)n_tokens * 4) ||
+        overlap(workspace, w.bytes, grad_out, gbytes) || overlap(workspace, w.bytes, ids, (size_t)n_tokens * 4) ||
         (valid && overlap(workspace, w.bytes, valid, n_tokens)))
         return fail(DLLM_ERR_ARG, "%s: grad_table or workspace overlaps another buffer", who);
     char *ws = (char *)workspace;
     const hipStream_t st = (hipStream_t)stream;
 
-    const Table table = {(char *)grad_table, table_stride * ts, n_vocab, D, lanes_of(D)};
-    const bool tb = table_dtype == DLLM_BF16;
+    const int nv = vectors_of(D);
+    const int fill = (D * ts + 15) / 16;
+    const Table table = {(char *)grad_table, table_stride * ts, n_vocab, D, nv, fill, log2_up(fill)};
+    const bool tb = table_dtype == DLLM_BF16, gb = grad_dtype == DLLM_BF16, old = accumulate != 0;
     SortParams S{};
     S.ids = ids; S.valid = valid;
     S.hist = (int32_t *)(ws + w.hist);
@@ -698,39 +786,37 @@ extern "C" dllm_status dllm_embed_grad(void *stream, const void *grad_out, int32
     S.bits = 1;                                // ids 0 .. n_vocab, n_vocab itself standing for no id
     while (n_vocab >> S.bits) ++S.bits;
     const int passes = (S.bits + kDigit - 1) / kDigit;
-    int filled = 0;
-    if (n_tokens > 0) {
-        // rows each sort launch clears, in whole filling workgroups
-        const int64_t row_bytes = (int64_t)D * ts, quota = accumulate ? 0 : (kFillBytes / row_bytes + kFillRows - 1) / kFillRows * kFillRows;
-        auto launch = [&](auto kernel, int sorting) {
-            S.fill_first = filled;
-            S.fill_end = filled = (int)std::min<int64_t>(n_vocab, filled + quota);
-            const int blocks = sorting + (S.fill_end - S.fill_first + kFillRows - 1) / kFillRows;
-            hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kSortThreads), 0, st, S);
-        };
-        if (w.tiles == 1) {
+    // every launch of the sort clears an even share of the table's rows
+    const bool one = w.tiles <= 1;
+    const int launches = one ? 1 : 2 * passes, at_once = rows_at_once(kSortThreads, table.fill_log2);
+    int launched = 0;
+    auto launch = [&](auto kernel, int sorting) {
+        S.fill_first = old ? 0 : (int)((int64_t)n_vocab * launched / launches);
+        S.fill_end = old ? 0 : (int)((int64_t)n_vocab * ++launched / launches);
+        const int blocks = sorting + (S.fill_end - S.fill_first + at_once - 1) / at_once;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kSortThreads), 0, st, S);
+    };
+    if (one) {
+        S.out = to;
+        tb ? launch(sort_one_kernel<true>, 1) : launch(sort_one_kernel<false>, 1);
+        std::swap(from, to);
+    } else {
+        for (int pass = 0; pass < passes; ++pass) {
+            S.shift = pass * kDigit;
             S.in = from;
             S.out = to;
-            tb ? launch(sort_one_kernel<true>, 1) : launch(sort_one_kernel<false>, 1);
-            if (passes & 1) std::swap(from, to);
-        } else {
-            for (int pass = 0; pass < passes; ++pass) {
-                S.shift = pass * kDigit;
-                S.in = from;
-                S.out = to;
-                if (pass == 0) {
-                    tb ? launch(sort_count_kernel<true, true>, w.tiles) : launch(sort_count_kernel<true, false>, w.tiles);
-                    tb ? launch(sort_move_kernel<true, true>, w.tiles) : launch(sort_move_kernel<true, false>, w.tiles);
-                } else {
-                    tb ? launch(sort_count_kernel<false, true>, w.tiles) : launch(sort_count_kernel<false, false>, w.tiles);
-                    tb ? launch(sort_move_kernel<false, true>, w.tiles) : launch(sort_move_kernel<false, false>, w.tiles);
-                }
-                std::swap(from, to);
+            if (pass == 0) {
+                tb ? launch(sort_count_kernel<true, true>, w.tiles) : launch(sort_count_kernel<true, false>, w.tiles);
+                tb ? launch(sort_move_kernel<true, true>, w.tiles) : launch(sort_move_kernel<true, false>, w.tiles);
+            } else {
+                tb ? launch(sort_count_kernel<false, true>, w.tiles) : launch(sort_count_kernel<false, false>, w.tiles);
+                tb ? launch(sort_move_kernel<false, true>, w.tiles) : launch(sort_move_kernel<false, false>, w.tiles);
             }
+            std::swap(from, to);
         }
-        rc = check_hip(hipGetLastError(), "dllm_embed_grad sort launch");
-        if (rc != DLLM_OK) return rc;
     }
+    rc = check_hip(hipGetLastError(), "dllm_embed_grad sort launch");
+    if (rc != DLLM_OK || n_tokens == 0) return rc;
 
     SumParams Q{};
     Q.grad = (const char *)grad_out;
@@ -743,19 +829,26 @@ extern "C" dllm_status dllm_embed_grad(void *stream, const void *grad_out, int32
     Q.n = n_tokens;
     Q.pieces = w.pieces;
     Q.colblocks = (D + kSumCols - 1) / kSumCols;
-    Q.accumulate = accumulate != 0;
-    Q.sum_blocks = (int)(((int64_t)Q.pieces * Q.colblocks + kSumWaves - 1) / kSumWaves);
-    Q.fill_first = filled;
+    Q.accumulate = old;
     Q.scale = scale;
-    const int blocks = Q.sum_blocks + (accumulate ? 0 : (n_vocab - filled + kFillRows - 1) / kFillRows);
-    if (blocks == 0) return DLLM_OK;
+    const int blocks = (int)(((int64_t)Q.pieces * Q.colblocks + kSumWaves - 1) / kSumWaves);
     auto sum = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, st, Q); };
-    if (grad_dtype == DLLM_BF16) tb ? sum(embed_sum_kernel<true, true>) : sum(embed_sum_kernel<true, false>);
-    else tb ? sum(embed_sum_kernel<false, true>) : sum(embed_sum_kernel<false, false>);
+    auto sum_of = [&](auto piece, auto with_old) {
+        constexpr int N = decltype(piece)::value;
+        constexpr bool O = decltype(with_old)::value;
+        if (gb) tb ? sum(embed_sum_kernel<true, true, N, O>) : sum(embed_sum_kernel<true, false, N, O>);
+        else tb ? sum(embed_sum_kernel<false, true, N, O>) : sum(embed_sum_kernel<false, false, N, O>);
+    };
+    typedef std::integral_constant<int, kPiece> Long;
+    typedef std::integral_constant<int, kSmallPiece> Short;
+    const bool small = w.piece == kSmallPiece;
+    if (old) small ? sum_of(Short(), std::true_type()) : sum_of(Long(), std::true_type());
+    else small ? sum_of(Short(), std::false_type()) : sum_of(Long(), std::false_type());
     rc = check_hip(hipGetLastError(), "dllm_embed_grad sum launch");
-    if (rc != DLLM_OK || n_tokens <= kPiece) return rc;      // no run longer than a piece
+    if (rc != DLLM_OK || n_tokens <= w.piece) return rc;     // no run longer than a piece
     const dim3 jg((unsigned)((D + kJoinCols - 1) / kJoinCols), kJoinRuns);
-    if (tb) hipLaunchKernelGGL(embed_join_kernel<true>, jg, dim3(256), 0, st, Q);
-    else hipLaunchKernelGGL(embed_join_kernel<false>, jg, dim3(256), 0, st, Q);
+    auto join = [&](auto kernel) { hipLaunchKernelGGL(kernel, jg, dim3(256), 0, st, Q); };
+    if (small) tb ? join(embed_join_kernel<true, kSmallPiece>) : join(embed_join_kernel<false, kSmallPiece>);
+    else tb ? join(embed_join_kernel<true, kPiece>) : join(embed_join_kernel<false, kPiece>);
     return check_hip(hipGetLastError(), "dllm_embed_grad join launch");
 }

@@ -573,7 +573,7 @@ struct GradParams {
     int32_t *status;
 };
 constexpr int kGradThreads = 256;
-constexpr int kGradVecs = 4;                   // vectors per thread
+constexpr int kGradVecs = 2;                   // vectors per thread: 158 us on 64 x 32 x 152064 bf16; 1: 197, 3: 161, 4: 168
 
 template <bool BF16, bool ENT>
 __global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(GradParams P) {
