@@ -167,9 +167,10 @@ struct Table {
 };
 
 // Rows a workgroup of `threads` clears: its threads lie along one row, or several narrow ones, one store
-// each for rows up to 16 bytes a thread.  One 16-byte store per thread in a dense sweep of the table writes
-// fastest: 6.3 TB/s over 1 GiB with 1024 threads, 5.6 with two stores, 5.5 with four.  Non-temporal, so the
-// zeros leave the last-level cache to the sums: 282 us for the whole gradient above, 312 with plain stores.
+// each for rows up to 16 bytes a thread.  What counts is that the stores in flight form a dense front in
+// the table: over 1.25 GB, one 16-byte store per thread in workgroups of 256 writes 6.6 TB/s, and 7.0 with
+// 33 to 40 KB of LDS each, which holds four of them on a compute unit; 1024 threads 6.0, two stores per
+// thread 5.9.  Non-temporal, so the zeros leave the last-level cache to the sums.
 constexpr int rows_at_once(int threads, int fill_log2) { return (1 << fill_log2) < threads ? threads >> fill_log2 : 1; }
 
 template <bool TB, int THREADS>
@@ -197,9 +198,10 @@ __device__ __forceinline__ void fill_rows(const Table &T, int first, int end) {
 // ---- sort ----------------------------------------------------------------------------------------
 constexpr int kDigit = 9;
 constexpr int kBins = 1 << kDigit;
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMinTile = 4096;                 // a multiple of kSortThreads
+// Threads of a sorting workgroup: kSortWide is the faster sort; kSortNarrow is the faster fill, where
+// the table is large enough for the fill to hide the sort (see launch).
+constexpr int kSortWide = 1024, kSortNarrow = 256;
+constexpr int kMinTile = 4096;                 // a multiple of 64 items per wave
 constexpr int kMaxTiles = 256;                 // a moving workgroup adds up the counts of the tiles before its own
 
 struct SortParams {
@@ -226,33 +228,33 @@ __device__ __forceinline__ uint64_t first_item(const SortParams &P, int i, bool 
     return (uint64_t)(uint32_t)id << 32 | (uint32_t)i;
 }
 template <bool FIRST>
-__device__ __forceinline__ uint64_t sort_item(const SortParams &P, const uint64_t *in, int i, bool report) {
+__device__ __forceinline__ uint64_t sort_item(const SortParams &P, int i, bool report) {
     if (FIRST) return first_item(P, i, report);
-    return in[i];
+    return P.in[i];
 }
 __device__ __forceinline__ int digit_of(uint64_t item, int shift) { return (int)((item >> 32) >> shift) & (kBins - 1); }
 
 // The filling workgroups of a sort launch follow its `sorting` ones.
-template <bool TB>
+template <bool TB, int T>
 __device__ __forceinline__ bool fills(const SortParams &P, int sorting) {
     if ((int)blockIdx.x < sorting) return false;
-    const int first = P.fill_first + ((int)blockIdx.x - sorting) * rows_at_once(kSortThreads, P.table.fill_log2);
-    fill_rows<TB, kSortThreads>(P.table, first, P.fill_end);
+    const int first = P.fill_first + ((int)blockIdx.x - sorting) * rows_at_once(T, P.table.fill_log2);
+    fill_rows<TB, T>(P.table, first, P.fill_end);
     return true;
 }
 
-template <bool FIRST, bool TB>
-__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortParams P) {
+template <bool FIRST, bool TB, int T>
+__global__ __launch_bounds__(T) void sort_count_kernel(SortParams P) {
     __shared__ int s_count[kBins];
-    if (fills<TB>(P, P.tiles)) return;
+    if (fills<TB, T>(P, P.tiles)) return;
     const int tid = threadIdx.x, tile = blockIdx.x;
     if (FIRST && tile == 0 && tid == 0) *P.n_long = 0;
-    if (tid < kBins) s_count[tid] = 0;
+    for (int b = tid; b < kBins; b += T) s_count[b] = 0;
     __syncthreads();
     const int i0 = tile * P.tile, end = min(P.n, i0 + P.tile);
-    for (int i = i0 + tid; i < end; i += kSortThreads) atomicAdd(&s_count[digit_of(sort_item<FIRST>(P, P.in, i, true), P.shift)], 1);
+    for (int i = i0 + tid; i < end; i += T) atomicAdd(&s_count[digit_of(sort_item<FIRST>(P, i, true), P.shift)], 1);
     __syncthreads();
-    if (tid < kBins) P.hist[tile * kBins + tid] = s_count[tid];
+    for (int b = tid; b < kBins; b += T) P.hist[tile * kBins + b] = s_count[b];
 }
 
 // Lanes of the wave that hold the same digit (only lanes with `on` count).
@@ -266,85 +268,109 @@ __device__ __forceinline__ uint64_t same_digit(int d, bool on) {
     return m;
 }
 
-// Where each wave's next item of each digit goes, from the waves' counts in s_at: after the items of
-// smaller digits (`total` of digit threadIdx.x in all), those of earlier tiles (`before`) and waves.
-__device__ __forceinline__ void place_digits(int before, int total, int (&s_at)[kSortWaves][kBins], int (&s_wave)[kBins / 64]) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int incl = 0;
-    if (tid < kBins) {
-        incl = wave_incl_scan(total);
-        if (lane == 63) s_wave[wave] = incl;
+// The counts of a workgroup's waves, and from them where each wave's next item of each digit goes.
+template <int T>
+struct Places {
+    static constexpr int kWaves = T / 64, kThreads = T < kBins ? T : kBins, kOwn = kBins / kThreads;
+    int at[kWaves][kBins];
+    int sum[kThreads / 64];
+
+    __device__ __forceinline__ void clear() {
+        for (int b = threadIdx.x; b < kWaves * kBins; b += T) (&at[0][0])[b] = 0;
     }
-    __syncthreads();
-    if (tid < kBins) {
-        int at = incl - total + before;
-        for (int w = 0; w < wave; ++w) at += s_wave[w];
+    // The first kThreads threads own kOwn digits each: `total` of them in all tiles, `before` in earlier ones.
+    // An item goes behind those of smaller digits, of earlier tiles and of earlier waves.
+    __device__ __forceinline__ void place(const int (&before)[kOwn], const int (&total)[kOwn]) {
+        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+        int all = 0, incl = 0;
+        if (tid < kThreads) {
 #pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) {
-            const int c = s_at[w][tid];
-            s_at[w][tid] = at;
-            at += c;
+            for (int o = 0; o < kOwn; ++o) all += total[o];
+            incl = wave_incl_scan(all);
+            if (lane == 63) sum[wave] = incl;
         }
+        __syncthreads();
+        if (tid < kThreads) {
+            int start = incl - all;
+            for (int w = 0; w < wave; ++w) start += sum[w];
+#pragma unroll
+            for (int o = 0; o < kOwn; ++o) {
+                int to = start + before[o];
+                start += total[o];
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    const int c = at[w][tid * kOwn + o];
+                    at[w][tid * kOwn + o] = to;
+                    to += c;
+                }
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-}
-// The place of this lane's item, the wave's lanes in order; `at` is the wave's row of s_at.
-__device__ __forceinline__ int take_place(int *at, int d, bool on) {
-    const uint64_t peers = same_digit(d, on);
-    const int rank = __popcll(peers & ((1ull << lane_id()) - 1));
-    int first = 0;
-    if (on) first = __atomic_load_n(&at[d], __ATOMIC_RELAXED);
-    // every lane has read its digit's place before the first lane of that digit moves it on
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (on && rank == 0) __atomic_store_n(&at[d], first + __popcll(peers), __ATOMIC_RELAXED);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    return first + rank;
-}
+    // The place of this lane's item, the wave's lanes in order.
+    __device__ __forceinline__ int take(int d, bool on) {
+        int *own = at[threadIdx.x >> 6];
+        const uint64_t peers = same_digit(d, on);
+        const int rank = __popcll(peers & ((1ull << lane_id()) - 1));
+        int first = 0;
+        if (on) first = __atomic_load_n(&own[d], __ATOMIC_RELAXED);
+        // every lane has read its digit's place before the first lane of that digit moves it on
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (on && rank == 0) __atomic_store_n(&own[d], first + __popcll(peers), __ATOMIC_RELAXED);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        return first + rank;
+    }
+};
 
 // Moves a tile's items; wave w moves consecutive ones, after those of waves < w.
-template <bool FIRST, bool TB>
-__global__ __launch_bounds__(kSortThreads) void sort_move_kernel(SortParams P) {
-    __shared__ int s_at[kSortWaves][kBins];
-    __shared__ int s_wave[kBins / 64];
-    if (fills<TB>(P, P.tiles)) return;
+template <bool FIRST, bool TB, int T>
+__global__ __launch_bounds__(T) void sort_move_kernel(SortParams P) {
+    typedef Places<T> Pl;
+    __shared__ Pl s;
+    if (fills<TB, T>(P, P.tiles)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, mine = blockIdx.x;
-    for (int b = tid; b < kSortWaves * kBins; b += kSortThreads) (&s_at[0][0])[b] = 0;
-    int before = 0, total = 0;
-    if (tid < kBins) {
+    s.clear();
+    int before[Pl::kOwn], total[Pl::kOwn];
+#pragma unroll
+    for (int o = 0; o < Pl::kOwn; ++o) before[o] = total[o] = 0;
+    if (tid < Pl::kThreads) {
 #pragma unroll 8
         for (int t = 0; t < P.tiles; ++t) {
-            const int c = P.hist[t * kBins + tid];
-            before += t < mine ? c : 0;
-            total += c;
+#pragma unroll
+            for (int o = 0; o < Pl::kOwn; ++o) {
+                const int c = P.hist[t * kBins + tid * Pl::kOwn + o];
+                before[o] += t < mine ? c : 0;
+                total[o] += c;
+            }
         }
     }
     __syncthreads();
-    const int share = P.tile / kSortWaves, w0 = mine * P.tile + wave * share;
+    const int share = P.tile / Pl::kWaves, w0 = mine * P.tile + wave * share;
     for (int i = w0 + lane; i < w0 + share; i += 64)
-        if (i < P.n) atomicAdd(&s_at[wave][digit_of(sort_item<FIRST>(P, P.in, i, false), P.shift)], 1);
+        if (i < P.n) atomicAdd(&s.at[wave][digit_of(sort_item<FIRST>(P, i, false), P.shift)], 1);
     __syncthreads();
-    place_digits(before, total, s_at, s_wave);
+    s.place(before, total);
     for (int i = w0 + lane; i - lane < w0 + share; i += 64) {
         const bool on = i < P.n;
-        const uint64_t item = on ? sort_item<FIRST>(P, P.in, i, false) : 0;
-        const int at = take_place(s_at[wave], digit_of(item, P.shift), on);
-        if (on) P.out[at] = item;
+        const uint64_t item = on ? sort_item<FIRST>(P, i, false) : 0;
+        const int to = s.take(digit_of(item, P.shift), on);
+        if (on) P.out[to] = item;
     }
 }
 
 // One tile: every pass in one workgroup, the items in LDS between the passes.
-constexpr int kHeld = kMinTile / kSortThreads;   // items per thread
-
 template <bool TB>
-__global__ __launch_bounds__(kSortThreads) void sort_one_kernel(SortParams P) {
-    __shared__ int s_at[kSortWaves][kBins];
-    __shared__ int s_wave[kBins / 64];
+__global__ __launch_bounds__(kSortWide) void sort_one_kernel(SortParams P) {
+    constexpr int T = kSortWide;
+    typedef Places<T> Pl;
+    constexpr int kHeld = kMinTile / T;        // items per thread
+    __shared__ Pl s;
     __shared__ uint64_t s_item[kMinTile];
-    if (fills<TB>(P, 1)) return;
+    if (fills<TB, T>(P, 1)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int share = P.tile / kSortWaves, w0 = wave * share;
+    const int share = P.tile / Pl::kWaves, w0 = wave * share;
     if (tid == 0) *P.n_long = 0;
     uint64_t item[kHeld];
 #pragma unroll
@@ -354,7 +380,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(SortParams P) {
         if (h * 64 < share && i < P.n) item[h] = first_item(P, i, true);
     }
     for (int shift = 0; shift < P.bits; shift += kDigit) {
-        for (int b = tid; b < kSortWaves * kBins; b += kSortThreads) (&s_at[0][0])[b] = 0;
+        s.clear();
         __syncthreads();
         if (shift > 0) {
 #pragma unroll
@@ -363,23 +389,27 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(SortParams P) {
         }
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
-            if (h * 64 < share && w0 + h * 64 + lane < P.n) atomicAdd(&s_at[wave][digit_of(item[h], shift)], 1);
+            if (h * 64 < share && w0 + h * 64 + lane < P.n) atomicAdd(&s.at[wave][digit_of(item[h], shift)], 1);
         __syncthreads();
-        int total = 0;
-        if (tid < kBins) {
+        int before[Pl::kOwn], total[Pl::kOwn];
 #pragma unroll
-            for (int w = 0; w < kSortWaves; ++w) total += s_at[w][tid];
+        for (int o = 0; o < Pl::kOwn; ++o) {
+            before[o] = total[o] = 0;
+            if (tid < Pl::kThreads) {
+#pragma unroll
+                for (int w = 0; w < Pl::kWaves; ++w) total[o] += s.at[w][tid * Pl::kOwn + o];
+            }
         }
-        place_digits(0, total, s_at, s_wave);
+        s.place(before, total);
         const bool last = shift + kDigit >= P.bits;
 #pragma unroll
         for (int h = 0; h < kHeld; ++h) {
             if (h * 64 >= share) continue;
             const bool on = w0 + h * 64 + lane < P.n;
-            const int at = take_place(s_at[wave], digit_of(item[h], shift), on);
+            const int to = s.take(digit_of(item[h], shift), on);
             if (on) {
-                if (last) P.out[at] = item[h];
-                else s_item[at] = item[h];
+                if (last) P.out[to] = item[h];
+                else s_item[to] = item[h];
             }
         }
         __syncthreads();
@@ -636,6 +666,10 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams P) {
 
 // ---- host -----------------------------------------------------------------------------------------
 constexpr int64_t kSmallUnits = 2048;
+// Table bytes from which the narrow sort's faster fill outweighs its slower sort: 1.25 GB take 288 us with
+// it against 301 (34816 tokens), 262 and 311 MB take 132 and 84 us against 115 and 75 (two batches of 8192
+// tokens, and 16384).
+constexpr int64_t kHidingFill = 768 << 20;
 
 struct GradSpace {
     size_t a, b, hist, n_long, long_piece, part, bytes;
@@ -643,8 +677,8 @@ struct GradSpace {
 };
 GradSpace grad_space(int64_t n, int64_t D) {
     GradSpace w{};
-    w.tile = (int)std::min<int64_t>(kMinTile, (n + kSortThreads - 1) / kSortThreads * kSortThreads);
-    if (w.tile == 0) w.tile = kSortThreads;
+    // whole rounds of 64 items for each wave of the wider sort
+    w.tile = (int)std::max<int64_t>(kSortWide, std::min<int64_t>(kMinTile, (n + kSortWide - 1) / kSortWide * kSortWide));
     while ((n + w.tile - 1) / w.tile > kMaxTiles) w.tile *= 2;
     w.tiles = (int)((n + w.tile - 1) / w.tile);
     // Fewer than kSmallUnits waves at kPiece tokens leave compute units idle while each wave works through
@@ -786,35 +820,44 @@ extern "C" dllm_status dllm_embed_grad(void *stream, const void *grad_out, int32
     S.bits = 1;                                // ids 0 .. n_vocab, n_vocab itself standing for no id
     while (n_vocab >> S.bits) ++S.bits;
     const int passes = (S.bits + kDigit - 1) / kDigit;
-    // every launch of the sort clears an even share of the table's rows
-    const bool one = w.tiles <= 1;
-    const int launches = one ? 1 : 2 * passes, at_once = rows_at_once(kSortThreads, table.fill_log2);
+    // Every launch of the sort clears an even share of the table's rows.
+    const bool one = w.tiles <= 1, narrow = !one && !old && (int64_t)n_vocab * D * ts >= kHidingFill;
+    const int launches = one ? 1 : 2 * passes;
+    const int at_once = rows_at_once(narrow ? kSortNarrow : kSortWide, table.fill_log2);
     int launched = 0;
-    auto launch = [&](auto kernel, int sorting) {
+    auto launch = [&](auto kernel, int threads, int sorting, size_t front) {
         S.fill_first = old ? 0 : (int)((int64_t)n_vocab * launched / launches);
         S.fill_end = old ? 0 : (int)((int64_t)n_vocab * ++launched / launches);
         const int blocks = sorting + (S.fill_end - S.fill_first + at_once - 1) / at_once;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kSortThreads), 0, st, S);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), front, st, S);
     };
-    if (one) {
-        S.out = to;
-        tb ? launch(sort_one_kernel<true>, 1) : launch(sort_one_kernel<false>, 1);
-        std::swap(from, to);
-    } else {
+    auto sort = [&](auto width, auto bf16) {
+        constexpr int T = decltype(width)::value;
+        constexpr bool B = decltype(bf16)::value;
+        // LDS on top of the kernel's own, for the fill's dense front
+        constexpr size_t count_front = T == kSortNarrow ? 32 << 10 : 0, move_front = T == kSortNarrow ? 25 << 10 : 0;
         for (int pass = 0; pass < passes; ++pass) {
             S.shift = pass * kDigit;
             S.in = from;
             S.out = to;
             if (pass == 0) {
-                tb ? launch(sort_count_kernel<true, true>, w.tiles) : launch(sort_count_kernel<true, false>, w.tiles);
-                tb ? launch(sort_move_kernel<true, true>, w.tiles) : launch(sort_move_kernel<true, false>, w.tiles);
+                launch(sort_count_kernel<true, B, T>, T, w.tiles, count_front);
+                launch(sort_move_kernel<true, B, T>, T, w.tiles, move_front);
             } else {
-                tb ? launch(sort_count_kernel<false, true>, w.tiles) : launch(sort_count_kernel<false, false>, w.tiles);
-                tb ? launch(sort_move_kernel<false, true>, w.tiles) : launch(sort_move_kernel<false, false>, w.tiles);
+                launch(sort_count_kernel<false, B, T>, T, w.tiles, count_front);
+                launch(sort_move_kernel<false, B, T>, T, w.tiles, move_front);
             }
             std::swap(from, to);
         }
-    }
+    };
+    typedef std::integral_constant<int, kSortNarrow> Narrow;
+    typedef std::integral_constant<int, kSortWide> Wide;
+    if (one) {
+        S.out = to;
+        tb ? launch(sort_one_kernel<true>, kSortWide, 1, 0) : launch(sort_one_kernel<false>, kSortWide, 1, 0);
+        std::swap(from, to);
+    } else if (tb) narrow ? sort(Narrow(), std::true_type()) : sort(Wide(), std::true_type());
+    else narrow ? sort(Narrow(), std::false_type()) : sort(Wide(), std::false_type());
     rc = check_hip(hipGetLastError(), "dllm_embed_grad sort launch");
     if (rc != DLLM_OK || n_tokens == 0) return rc;
 
