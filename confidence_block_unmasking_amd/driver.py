@@ -11,7 +11,9 @@
 
 The driver owns the device buffers and the loop rule only; pack, step and compact run in
 libdllm.so.  The model forward is not part of this library: the caller passes `forward`, which
-fills the session's logits buffer for the current box (a synthetic generator in tests/bench).
+fills the session's logits buffer for the current box (a synthetic generator in tests/bench); it may
+start from the box's embeddings (Session.embed).  A session can keep the log probabilities, entropies
+and top alternatives of the tokens it generates (Session.record_logprobs).
 Per step the only device-to-host traffic is the done flags and the new mask of the box rows.
 """
 from __future__ import annotations
@@ -52,6 +54,7 @@ class Session:
         p64 = np.asarray(p, np.int64)
         K64 = np.asarray(K, np.int64)
         self.W_max = int((p64 + K64 * self.L).max()) if len(p64) else self.L
+        self.K_max = int(K64.max()) if len(K64) else 1
         n = self.rows_cap
         i32, u8, f32 = torch.int32, torch.uint8, torch.float32
         self.box_ids = torch.empty(n * self.W_max, dtype=i32, device=device)
@@ -79,6 +82,7 @@ class Session:
         self._h_mask = torch.empty(n * self.L, dtype=u8, pin_memory=pin)
         self._h_status = torch.empty(1, dtype=i32, pin_memory=pin)
         self.logits = logits if logits is not None else torch.empty((n, self.L, self.V), dtype=dtype, device=device)
+        self.record = None                           # per-token log probabilities (record_logprobs)
         self.W = 0
         self.stats = dict(steps=0, request_steps=0, positions_scored=0, compacts=0, packs=0, rounds=0,
                           idle_request_steps=0, max_cost=0, evicted=0, admitted=0, unmasked=0,
@@ -183,6 +187,57 @@ class Session:
                                self.features_buf, self.status)
         return self.features_buf[:self.rows * api.N_FEATURES].view(self.rows, api.N_FEATURES)
 
+    # ---- the two sides of the forward -------------------------------------------------------------
+    def embed(self, table, scale=1.0, out=None):
+        """The current box's embeddings [rows, W, D] from `table` [n_vocab, D] (n_vocab > mask_id), zeros
+        in the padding, for a forward to start from.  out: a buffer for them (any float type), or
+        a new tensor of the table's type."""
+        D = table.shape[1]
+        if out is None:
+            out = torch.empty((self.rows, self.W, D), dtype=table.dtype, device=self.device)
+        n = self.rows * self.W
+        api.dllm_embed(table, self.box_ids[:n], out, self.status, valid=self.box_valid[:n], scale=scale)
+        return out
+
+    def record_logprobs(self, k=0):
+        """Keep, from now on, the log probability, entropy and k top alternatives of every token a step
+        unmasks (read back with logprobs())."""
+        n, dev = self.reqs.n_req * self.K_max, self.device
+        nan = float("nan")
+        rec = dict(logprob=torch.full((n, self.L), nan, dtype=torch.float32, device=dev),
+                   entropy=torch.full((n, self.L), nan, dtype=torch.float32, device=dev))
+        if k > 0:
+            rec["top_ids"] = torch.full((n, self.L, k), -1, dtype=torch.int32, device=dev)
+            rec["top_logprobs"] = torch.full((n, self.L, k), nan, dtype=torch.float32, device=dev)
+        self.record = rec
+        self.record_k = int(k)
+        self._record_rows = {name: torch.empty((self.rows_cap, *t.shape[1:]), dtype=t.dtype, device=dev)
+                             for name, t in rec.items()}
+        self._record_ws = api.new_logprobs_workspace(self.rows_cap, self.L, self.V, k, self.dtype, device=dev)
+
+    def _record_step(self):
+        """The tokens the last step unmasked: its rows' blocks out of the record, the new entries
+        written, and back.  Everything stays on the stream."""
+        n = self.rows
+        at = self.row_req[:n].long() * self.K_max + self.b_rows[:n]
+        rows = {name: t[:n] for name, t in self._record_rows.items()}
+        for name, t in self.record.items():
+            torch.index_select(t, 0, at, out=rows[name])
+        api.dllm_logprobs(self.logits, self.masks[1 - self.cur], self.box()[:, self.W - self.L:], rows["logprob"],
+                          self._record_ws, self.status, entropy=rows["entropy"], top_ids=rows.get("top_ids"),
+                          top_logprobs=rows.get("top_logprobs"), exclude=self.masks[self.cur], rows=n, L=self.L,
+                          V=self.V, pos_stride=self.V, row_stride=self.L * self.V)
+        for name, t in self.record.items():
+            t.index_copy_(0, at, rows[name])
+
+    def logprobs(self):
+        """The record by request and generated position: logprob and entropy [n_req, K_max*L] (NaN where
+        no token was unmasked), and with alternatives top_ids (-1) and top_logprobs [n_req, K_max*L, k]."""
+        if self.record is None:
+            raise ValueError("record_logprobs() was not called")
+        n = self.reqs.n_req
+        return {name: t.view(n, self.K_max * self.L, *t.shape[2:]) for name, t in self.record.items()}
+
     # ---- the loop rule ----------------------------------------------------------------------------
     def run(self, mode, forward, max_steps=10**7, on_step=None, timed=False, max_rounds=0, metrics=False,
             step_fn=None):
@@ -224,6 +279,8 @@ class Session:
                     step_fn(self, int(masked.sum()))
                 else:
                     self.step(timed=timed, report=metrics)
+                if self.record is not None:
+                    self._record_step()
                 done, mask_host, st = self._readback()
                 if st != 0:
                     raise api.DllmError(st, "dllm_step", "(device status)")
@@ -259,6 +316,9 @@ class Session:
         compact): the request table, token arena, block masks, row map, queue and active rows, plus
         the fixed parameters.  The box, per-row views and step buffers are rebuilt by the next pack."""
         h = self.host_table()
+        if self.record is not None:
+            h["record"] = {name: t.cpu().numpy() for name, t in self.record.items()}
+            h["record_k"] = self.record_k
         return dict(h, rows=self.rows, L=self.L, V=self.V, dtype=self.dtype, rows_cap=self.rows_cap,
                     budget=self.budget, mask_id=self.mask_id, pad_id=self.pad_id, eos_id=self.eos_id)
 
@@ -266,11 +326,16 @@ class Session:
     def from_snapshot(cls, snap, device="cuda", logits=None):
         """A session that continues from snapshot(): run() then carries on where the other stopped
         (its opening admission admits nothing the last compact did not)."""
-        return cls(snap["p"], snap["K"], snap["b"], snap["state"], snap["threshold"], snap["arena_off"],
-                   snap["arena"], snap["blk_mask"], snap["row_req"], snap["rows"], snap["queue"], L=snap["L"],
-                   V=snap["V"], dtype=snap["dtype"], rows_cap=snap["rows_cap"], budget=snap["budget"],
-                   mask_id=snap["mask_id"], pad_id=snap["pad_id"], eos_id=snap["eos_id"], device=device,
-                   logits=logits)
+        s = cls(snap["p"], snap["K"], snap["b"], snap["state"], snap["threshold"], snap["arena_off"],
+                snap["arena"], snap["blk_mask"], snap["row_req"], snap["rows"], snap["queue"], L=snap["L"],
+                V=snap["V"], dtype=snap["dtype"], rows_cap=snap["rows_cap"], budget=snap["budget"],
+                mask_id=snap["mask_id"], pad_id=snap["pad_id"], eos_id=snap["eos_id"], device=device,
+                logits=logits)
+        if "record" in snap:
+            s.record_logprobs(snap["record_k"])
+            for name, t in s.record.items():
+                t.copy_(torch.as_tensor(snap["record"][name]))
+        return s
 
     # ---- host views for tests -----------------------------------------------------------------
     def host_table(self):
