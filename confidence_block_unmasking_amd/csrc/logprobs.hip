@@ -27,6 +27,9 @@
 //     that reach the bound (about 25 of 2432 for k = 20 and V = 152064), and puts each of their
 //     elements above the bound into its place by counting the ones before it.
 //     Keeping sorted lists in the streaming kernel instead took 2.3 times as long.
+#include <algorithm>
+#include <type_traits>
+
 #include "elem_common.h"
 
 namespace {
@@ -137,21 +140,15 @@ __device__ __forceinline__ int kth_floor(int key, int k) {
     return t == 0 ? kNoKey : (int)(t ^ 0x80000000u) - 1;
 }
 
-// Kernel 1: one record per chunk of every selected slot, and its lanes' maxima.
-template <bool BF16, bool ENT, bool TOP>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void logprob_chunks_kernel(LogprobParams P) {
-    extern __shared__ int s_id[];              // [win] selected slots of this workgroup's window
-    __shared__ int s_tmp[2][kWaves];
-    __shared__ int s_next;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = uni(tid >> 6);
-    const int L = P.L, S = P.rows * L, NC = P.NC;
-    const int ntiles = (S + kTile - 1) / kTile;
-
-    // 0. Number the selected slots in slot order (16 per thread and tile), split their chunks evenly
-    //    over the workgroups and list this workgroup's slots in LDS.
+// Number the selected slots in slot order (16 per thread and tile) and list in s_id those of this
+// workgroup, numbers q_lo .. q_hi that range(M, q_lo, q_hi) gives for M selected slots; false if it gives
+// none.  The caller's next barrier makes the list visible.
+template <typename Range>
+__device__ __forceinline__ bool list_slots(const LogprobParams &P, int *s_id, int (&s_tmp)[2][kWaves], Range range) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+    const int S = P.rows * P.L, ntiles = (S + kTile - 1) / kTile;
     const uint32_t mb0 = selected16(P, tid * 16, S);
-    fetch_args(P.logits, P.row_stride_b, P.pos_stride_b, P.partials, P.lane_max, P.V);
+    fetch_args(P.logits, P.row_stride_b, P.pos_stride_b, P.partials, P.lane_max, P.V, P.NC);
     int more_cnt = 0;
     for (int t = 1; t < ntiles; ++t) more_cnt += __popc(selected16(P, t * kTile + tid * 16, S));
     // slots selected before this thread's 16 in its tile, and in the whole tile
@@ -173,13 +170,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
     place(mb0, s_tmp[0], before, base);
     int M = base;
     if (ntiles > 1) M += block_sum(more_cnt, s_tmp[1]);
-    M = uni(M);
-    const int I = M * NC;                      // chunk t is chunk t % NC of selected slot t / NC
-    const int G = gridDim.x, g = blockIdx.x;
-    const int per = I / G, rem = I - per * G;
-    const int t0 = g * per + min(g, rem), t1 = t0 + per + (g < rem ? 1 : 0);
-    if (t0 >= t1) return;                      // uniform over the workgroup
-    const int q_lo = t0 / NC, q_hi = (t1 - 1) / NC;
+    int q_lo, q_hi;
+    if (!range(uni(M), q_lo, q_hi)) return false;      // uniform over the workgroup
     auto list = [&](uint32_t mb, int q, int s0) {
         for (; mb != 0 && q <= q_hi; ++q) {
             if (q >= q_lo) s_id[q - q_lo] = s0 + __builtin_ctz(mb);
@@ -195,18 +187,81 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
         list(mb, base + before, t * kTile + tid * 16);
         base += total;
     }
+    return true;
+}
+__device__ __forceinline__ const char *slot_row(const LogprobParams &P, int slot) {
+    const int r = slot / P.L, j = slot - r * P.L;
+    return P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
+}
+
+// A chunk's record {max, sum, weighted sum} from its values, which it may overwrite; lm: this lane's
+// largest value.
+template <int E, bool ENT>
+__device__ __forceinline__ float4 chunk_record(float (&x)[kVPL][E], float &lm) {
+    lm = x[0][0];
+#pragma unroll
+    for (int kk = 0; kk < kVPL; ++kk) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) lm = fmaxf(lm, x[kk][e]);
+    }
+    const float m = red_max_bc(lm);
+    float near = m;                            // what the FMA takes off
+    if (!(fabsf(m) <= kNearMax)) {             // far from 0, or no finite logit: subtract first
+        near = 0.0f;
+        if (m != -INFINITY) {
+#pragma unroll
+            for (int kk = 0; kk < kVPL; ++kk) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[kk][e] -= m;
+            }
+        }
+    }
+    const float nml = -near * kLog2e;
+    float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, w4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kk = 0; kk < kVPL; ++kk) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float y = fmaf(x[kk][e], kLog2e, nml);
+            const float p = __builtin_amdgcn_exp2f(y);
+            s4[e % 4] += p;
+            if (ENT) w4[e % 4] = fmaf(p, fmaxf(y, kFarBelow), w4[e % 4]);
+        }
+    }
+    const float r = fmaf(near, kLog2e, nml);   // what rounding nml added to every y
+    const float back = __builtin_amdgcn_exp2f(-r);
+    const float s1 = red_sum_bc((s4[0] + s4[1]) + (s4[2] + s4[3]));
+    const float w = ENT ? fmaf(-r, s1, red_sum_bc((w4[0] + w4[1]) + (w4[2] + w4[3]))) * back : 0.0f;
+    return make_float4(m, s1 * back, w, 0.0f);
+}
+
+// Kernel 1: one record per chunk of every selected slot, and its lanes' maxima.
+template <bool BF16, bool ENT, bool TOP>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void logprob_chunks_kernel(LogprobParams P) {
+    extern __shared__ int s_id[];              // [win] selected slots of this workgroup's window
+    __shared__ int s_tmp[2][kWaves];
+    __shared__ int s_next;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = uni(tid >> 6);
+    const int NC = P.NC;
+    int t0 = 0, t1 = 0, q_lo = 0;              // chunk t is chunk t % NC of selected slot t / NC
+    if (!list_slots(P, s_id, s_tmp, [&](int M, int &lo, int &hi) {
+            const int I = M * NC, G = gridDim.x, g = blockIdx.x;
+            const int per = I / G, rem = I - per * G;
+            t0 = g * per + min(g, rem), t1 = t0 + per + (g < rem ? 1 : 0);
+            if (t0 >= t1) return false;
+            lo = q_lo = t0 / NC, hi = (t1 - 1) / NC;
+            return true;
+        }))
+        return;
     if (tid == 0) s_next = t0 + kWaves;
     __syncthreads();
 
-    // 1. Chunks: wave w starts with chunk t0 + w, then takes the next untaken one.
+    // Wave w starts with chunk t0 + w, then takes the next untaken one.
     int t = t0 + wave;
     if (t >= t1) return;                       // no barrier follows
     constexpr int E = Fmt<BF16>::E;
     const int V = P.V, full = V / E;           // whole vectors of a row
-    auto row_of = [&](int s) -> const char * {
-        const int r = s / L, j = s - r * L;
-        return P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
-    };
     auto whole = [&](int c) { return min(max(full - c * kCH, 0), kCH); };
     // lane i holds the wave's i-th pending record: a store between loads would hold every later load
     // back until it completed, so records leave 64 at a time
@@ -214,7 +269,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
     int pend_at = 0, npend = 0;
     int q = uni(t / NC), c = t - q * NC;
     int slot = uni(s_id[q - q_lo]);
-    const char *row = row_of(slot);
+    const char *row = slot_row(P, slot);
     u32x4 raw[kVPL];
     issue_chunk<BF16>(raw, row, c * kCH, whole(c), V);
     while (true) {
@@ -229,53 +284,19 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
         if (more) {
             if (qn != q) {
                 slot = uni(s_id[qn - q_lo]);
-                row = row_of(slot);
+                row = slot_row(P, slot);
             }
             issue_chunk<BF16>(raw, row, cn * kCH, whole(cn), V);
         }
-        float lm = x[0][0];
-#pragma unroll
-        for (int kk = 0; kk < kVPL; ++kk) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) lm = fmaxf(lm, x[kk][e]);
-        }
-        const float m = red_max_bc(lm);
+        float lm;
+        const float4 rec = chunk_record<E, ENT>(x, lm);
         if (TOP) {
             char *to = P.lane_max + (int64_t)at * (64 * (16 / E));
             if (BF16) ((uint16_t *)to)[lane] = (uint16_t)(__float_as_uint(lm) >> 16);
             else ((float *)to)[lane] = lm;
         }
-
-        float near = m;                        // what the FMA takes off
-        if (!(fabsf(m) <= kNearMax)) {         // far from 0, or no finite logit: subtract first
-            near = 0.0f;
-            if (m != -INFINITY) {
-#pragma unroll
-                for (int kk = 0; kk < kVPL; ++kk) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[kk][e] -= m;
-                }
-            }
-        }
-        const float nml = -near * kLog2e;
-        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, w4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int kk = 0; kk < kVPL; ++kk) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float y = fmaf(x[kk][e], kLog2e, nml);
-                const float p = __builtin_amdgcn_exp2f(y);
-                s4[e % 4] += p;
-                if (ENT) w4[e % 4] = fmaf(p, fmaxf(y, kFarBelow), w4[e % 4]);
-            }
-        }
-        const float r = fmaf(near, kLog2e, nml);           // what rounding nml added to every y
-        const float back = __builtin_amdgcn_exp2f(-r);
-        const float s1 = red_sum_bc((s4[0] + s4[1]) + (s4[2] + s4[3]));
-        const float s = s1 * back;
-        const float w = ENT ? fmaf(-r, s1, red_sum_bc((w4[0] + w4[1]) + (w4[2] + w4[3]))) * back : 0.0f;
         if (lane == npend) {
-            pend = make_float4(m, s, w, 0.0f);
+            pend = rec;
             pend_at = at;
         }
         if (++npend == 64 || !more) {
@@ -319,10 +340,6 @@ __device__ __forceinline__ Softmax join_records(const float4 *rec, int NC, float
     const float ls = logf(s);
     return {mw, ls, fmaf(-kLn2, w / s, ls)};
 }
-__device__ __forceinline__ const char *slot_row(const LogprobParams &P, int slot) {
-    const int r = slot / P.L, j = slot - r * P.L;
-    return P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
-}
 // The given token's column; -1 for none, or one out of range.
 __device__ __forceinline__ int given_token(const LogprobParams &P, int slot) {
     if (P.tokens == nullptr) return -1;
@@ -365,66 +382,48 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprob_join_kernel(LogprobPa
     if (lane_id() == 0) write_slot(P, slot, f, tok, x);
 }
 
-// Kernel 2, with alternatives: one workgroup per slot.
-constexpr int kTopThreads = 64 * kJoinWaves;
-constexpr int kTopChunks = 20;                 // chunks per wave whose maxima stay in registers
+// ---- alternatives of one slot, by a workgroup of WAVES ---------------------------------------------
+constexpr int kTopChunks = 10;                 // chunks per wave whose maxima stay in registers
 constexpr int kTopShares = 256;                // lane shares, and elements, the quick way has room for
 
-template <bool BF16>
-__global__ __launch_bounds__(kTopThreads) void logprob_top_kernel(LogprobParams P) {
-    typedef typename Row<BF16>::vec vec;
-    constexpr int E = Fmt<BF16>::E;
-    __shared__ int s_group[kJoinWaves][64];
-    __shared__ int s_share[kTopShares];
-    __shared__ int2 s_elem[kTopShares];
-    __shared__ int s_n[2];                     // shares, elements
-    __shared__ float s_f[2];
-    const int tid = threadIdx.x, lane = lane_id(), wave = uni(tid >> 6);
-    const int slot = blockIdx.x, NC = P.NC, V = P.V, k = P.k;
-    fetch_args(P.mask, P.exclude, P.partials, P.lane_max, P.tokens, P.token_stride, P.logits, P.NC, P.V, P.k);
-    const int tok = given_token(P, slot);
-    if (!selected(P, slot)) return;
-    const char *row = slot_row(P, slot);
-    const float4 *rec = P.partials + (int64_t)slot * NC;
-    // the last wave also joins the records: its loads go out now, their use waits for a quiet moment
-    const bool joins = wave == kJoinWaves - 1;
-    float4 first = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float xt = 0.0f;
-    if (joins) {
-        first = rec[min(lane, NC - 1)];
-        if (tok >= 0) xt = logit_at<BF16>(row, tok);
-    }
-    if (tid < 2) s_n[tid] = 0;
+template <int WAVES>
+struct TopShared {
+    int group[WAVES][64];
+    int share[kTopShares];
+    int2 elem[kTopShares];
+    int n[2];                                  // shares, elements
+    float m, ls;
+};
 
-    // Wave w holds chunks w, w + 4, ...: keys of this lane's maxima.  Lane l's maxima form group l; the
-    // k-th largest of the 64 group maxima is a lower bound of the k-th largest element.
+// key_of(c): the key of this lane's largest element of chunk c; softmax(): the slot's softmax, asked of the
+// last wave only, late.
+template <bool BF16, int WAVES, typename KeyOf, typename SoftmaxOf>
+__device__ __forceinline__ void top_of_slot(const LogprobParams &P, TopShared<WAVES> &sh, int slot, const char *row, KeyOf key_of,
+                                            SoftmaxOf softmax) {
+    typedef typename Row<BF16>::vec vec;
+    constexpr int E = Fmt<BF16>::E, kSpan = kTopChunks * WAVES;
+    const int tid = threadIdx.x, lane = lane_id(), wave = uni(tid >> 6), NC = P.NC, V = P.V, k = P.k;
+    if (tid < 2) sh.n[tid] = 0;
+    // Wave w holds chunks w, w + WAVES, ...  Lane l's maxima form group l; the k-th largest of the 64 group
+    // maxima is a lower bound of the k-th largest element.
     int key[kTopChunks];
     auto load_keys = [&](int c0) {
-        const char *lm = P.lane_max + ((int64_t)slot * NC) * (64 * (16 / E));
 #pragma unroll
         for (int i = 0; i < kTopChunks; ++i) {
-            const int c = c0 + i * kJoinWaves + wave;
-            key[i] = kNoKey;
-            if (c < NC) {
-                const int64_t at = (int64_t)c * 64 + lane;
-                key[i] = BF16 ? (int)((const uint16_t *)lm)[at] << 16 : ((const int *)lm)[at];
-            }
+            const int c = c0 + i * WAVES + wave;
+            key[i] = c < NC ? key_of(c) : kNoKey;
         }
-#pragma unroll
-        for (int i = 0; i < kTopChunks; ++i)
-            if (c0 + i * kJoinWaves + wave < NC) key[i] = order_key(__int_as_float(key[i]));
     };
-    constexpr int kSpan = kTopChunks * kJoinWaves;
     int group = kNoKey;
     for (int c0 = 0; c0 < NC; c0 += kSpan) {
         load_keys(c0);
 #pragma unroll
         for (int i = 0; i < kTopChunks; ++i) group = max(group, key[i]);
     }
-    s_group[wave][lane] = group;
+    sh.group[wave][lane] = group;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kJoinWaves; ++w) group = max(group, s_group[w][lane]);
+    for (int w = 0; w < WAVES; ++w) group = max(group, sh.group[w][lane]);
     const int floor = kth_floor(group, k);
 
     // Room for `mine` entries of this thread in a shared list: one atomic per wave.
@@ -440,19 +439,19 @@ __global__ __launch_bounds__(kTopThreads) void logprob_top_kernel(LogprobParams 
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < kTopChunks; ++i) mine += key[i] > floor;
-        int at = room(mine, &s_n[0]);
+        int at = room(mine, &sh.n[0]);
         if (__ballot(mine > 0) != 0) {
 #pragma unroll
             for (int i = 0; i < kTopChunks; ++i) {
                 if (key[i] > floor) {
-                    if (at < kTopShares) s_share[at] = (c0 + i * kJoinWaves + wave) * 64 + lane;
+                    if (at < kTopShares) sh.share[at] = (c0 + i * WAVES + wave) * 64 + lane;
                     ++at;
                 }
             }
         }
     }
     __syncthreads();
-    const int shares = s_n[0];
+    const int shares = sh.n[0];
     auto load_share = [&](int share, int kk, float (&x)[E], int &col) {
         const int v = (share >> 6) * kCH + kk * 64 + (share & 63);
         col = v * E;
@@ -465,46 +464,45 @@ __global__ __launch_bounds__(kTopThreads) void logprob_top_kernel(LogprobParams 
     };
     // Their elements above the bound: at least k, with few more unless many logits are equal.
     if (shares <= kTopShares) {
-        for (int i0 = wave * 64; i0 < shares * kVPL; i0 += kTopThreads) {
+        for (int i0 = wave * 64; i0 < shares * kVPL; i0 += 64 * WAVES) {
             const int i = i0 + lane;
             float x[E];
             int col = V, mine = 0;
-            if (i < shares * kVPL) load_share(s_share[i / kVPL], i % kVPL, x, col);
+            if (i < shares * kVPL) load_share(sh.share[i / kVPL], i % kVPL, x, col);
             int ek[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 ek[e] = col + e < V ? order_key(x[e]) : kNoKey;
                 mine += ek[e] > floor;
             }
-            int at = room(mine, &s_n[1]);
+            int at = room(mine, &sh.n[1]);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 if (ek[e] > floor) {
-                    if (at < kTopShares) s_elem[at] = make_int2(ek[e], col + e);
+                    if (at < kTopShares) sh.elem[at] = make_int2(ek[e], col + e);
                     ++at;
                 }
             }
         }
     }
-    if (joins) {
-        const Softmax f = join_records(rec, NC, first);
+    if (wave == WAVES - 1) {
+        const Softmax f = softmax();
         if (lane == 0) {
-            write_slot(P, slot, f, tok, xt);
-            s_f[0] = f.m;
-            s_f[1] = f.ls;
+            sh.m = f.m;
+            sh.ls = f.ls;
         }
     }
     __syncthreads();
-    const int elems = s_n[1];
-    const float m = s_f[0], ls = s_f[1];
+    const int elems = sh.n[1];
+    const float m = sh.m, ls = sh.ls;
     if (shares <= kTopShares && elems <= kTopShares) {
-    // an element's place is the number of elements before it in the full order
+        // an element's place is the number of elements before it in the full order
         if (tid < elems) {
-            const int2 own = s_elem[tid];
+            const int2 own = sh.elem[tid];
             int place = 0;
 #pragma unroll 4
             for (int i = 0; i < elems; ++i) {
-                const int2 o = s_elem[i];
+                const int2 o = sh.elem[i];
                 place += o.x > own.x || (o.x == own.x && o.y < own.y);
             }
             if (place < k) {
@@ -512,44 +510,115 @@ __global__ __launch_bounds__(kTopThreads) void logprob_top_kernel(LogprobParams 
                 P.top_lp[(int64_t)slot * k + place] = (key_value(own.x) - m) - ls;
             }
         }
-        return;
-    }
-    // Many logits equal to the k-th: wave 0 inserts share after share into a list sorted across its
-    // lanes.  Columns of a chunk lie above every column of the chunks before it, so once the list is
-    // full a share has to exceed its last entry, and the first chunks settle it.
-    if (wave != 0) return;
-    Best b = {kNoKey, 0x7FFFFFFF, kNoKey};
-    int cut_col = 0x7FFFFFFF;
-    const char *lm = P.lane_max + ((int64_t)slot * NC) * (64 * (16 / E));
-    for (int c = 0; c < NC; ++c) {
-        const int64_t at = (int64_t)c * 64 + lane;
-        const int ck = order_key(BF16 ? __uint_as_float((uint32_t)((const uint16_t *)lm)[at] << 16) : ((const float *)lm)[at]);
-        const bool on = ck > max(floor, b.cut);
-        if (__ballot(on) == 0) continue;
+    } else if (wave == 0) {
+        // Many logits equal to the k-th: one wave inserts share after share into a list sorted across its
+        // lanes.  Columns of a chunk lie above every column of the chunks before it, so once the list is
+        // full a share has to exceed its last entry, and the first chunks settle it.
+        Best b = {kNoKey, 0x7FFFFFFF, kNoKey};
+        int cut_col = 0x7FFFFFFF;
+        for (int c = 0; c < NC; ++c) {
+            const bool on = key_of(c) > max(floor, b.cut);
+            if (__ballot(on) == 0) continue;
 #pragma unroll 1
-        for (int kk = 0; kk < kVPL; ++kk) {
-            float x[E];
-            int col = V;
-            if (on) load_share(c * 64 + lane, kk, x, col);
+            for (int kk = 0; kk < kVPL; ++kk) {
+                float x[E];
+                int col = V;
+                if (on) load_share(c * 64 + lane, kk, x, col);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int ek = col + e < V ? order_key(x[e]) : kNoKey;
-                uint64_t in = __ballot(ek > floor && (ek > b.cut || (ek == b.cut && col + e < cut_col)));
-                while (in != 0) {
-                    const int l = __builtin_ctzll(in);
-                    const int nk = __builtin_amdgcn_readlane(ek, l), nc = __builtin_amdgcn_readlane(col + e, l);
-                    insert_at(b, __popcll(__ballot(b.key > nk || (b.key == nk && b.col < nc))), nk, nc, k);
-                    cut_col = __builtin_amdgcn_readlane(b.col, k - 1);
-                    in &= in - 1;
-                    in &= __ballot(ek > b.cut || (ek == b.cut && col + e < cut_col));
+                for (int e = 0; e < E; ++e) {
+                    const int ek = col + e < V ? order_key(x[e]) : kNoKey;
+                    uint64_t in = __ballot(ek > floor && (ek > b.cut || (ek == b.cut && col + e < cut_col)));
+                    while (in != 0) {
+                        const int l = __builtin_ctzll(in);
+                        const int nk = __builtin_amdgcn_readlane(ek, l), nc = __builtin_amdgcn_readlane(col + e, l);
+                        insert_at(b, __popcll(__ballot(b.key > nk || (b.key == nk && b.col < nc))), nk, nc, k);
+                        cut_col = __builtin_amdgcn_readlane(b.col, k - 1);
+                        in &= in - 1;
+                        in &= __ballot(ek > b.cut || (ek == b.cut && col + e < cut_col));
+                    }
                 }
             }
         }
+        if (lane < k) {
+            P.top_ids[(int64_t)slot * k + lane] = b.col;
+            P.top_lp[(int64_t)slot * k + lane] = (key_value(b.key) - m) - ls;
+        }
     }
-    if (lane < k) {
-        P.top_ids[(int64_t)slot * k + lane] = b.col;
-        P.top_lp[(int64_t)slot * k + lane] = (key_value(b.key) - m) - ls;
+}
+
+// Kernel 2, with alternatives: one workgroup per slot.
+template <bool BF16>
+__global__ __launch_bounds__(64 * kJoinWaves) void logprob_top_kernel(LogprobParams P) {
+    __shared__ TopShared<kJoinWaves> sh;
+    const int lane = lane_id(), slot = blockIdx.x, NC = P.NC;
+    fetch_args(P.mask, P.exclude, P.partials, P.lane_max, P.tokens, P.token_stride, P.logits, P.NC, P.V, P.k);
+    const int tok = given_token(P, slot);
+    if (!selected(P, slot)) return;
+    const char *row = slot_row(P, slot);
+    const float4 *rec = P.partials + (int64_t)slot * NC;
+    // the last wave also joins the records: its loads go out now, their use waits for a quiet moment
+    float4 first = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float xt = 0.0f;
+    if (uni(threadIdx.x >> 6) == kJoinWaves - 1) {
+        first = rec[min(lane, NC - 1)];
+        if (tok >= 0) xt = logit_at<BF16>(row, tok);
     }
+    const char *lm = P.lane_max + (int64_t)slot * NC * (64 * (BF16 ? 2 : 4));
+    top_of_slot<BF16>(
+        P, sh, slot, row,
+        [&](int c) {
+            const int64_t at = (int64_t)c * 64 + lane;
+            return order_key(BF16 ? __uint_as_float((uint32_t)((const uint16_t *)lm)[at] << 16) : ((const float *)lm)[at]);
+        },
+        [&]() {
+            const Softmax f = join_records(rec, NC, first);
+            if (lane == 0) write_slot(P, slot, f, tok, xt);
+            return f;
+        });
+}
+
+// ---- one kernel -----------------------------------------------------------------------------------
+// For few short rows: a workgroup per slot.  Its waves take the slot's chunks in turn, keep records and lane
+// maxima in LDS, and finish the slot there (the same arithmetic in the same order: the same bits), which
+// saves the second launch and the mask scan.
+constexpr int kShortRow = 16;                  // chunks of a row at most
+
+template <bool BF16, bool ENT, bool TOP>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void logprob_rows_kernel(LogprobParams P) {
+    __shared__ float4 s_rec[kShortRow];
+    __shared__ int s_key[TOP ? kShortRow : 1][64];
+    __shared__ TopShared<kWaves> sh;
+    const int lane = lane_id(), wave = uni(threadIdx.x >> 6), slot = blockIdx.x;
+    fetch_args(P.mask, P.exclude, P.tokens, P.token_stride, P.logits, P.row_stride_b, P.pos_stride_b, P.NC, P.V, P.k);
+    const int tok = given_token(P, slot);
+    if (!selected(P, slot)) return;
+    const int NC = P.NC, V = P.V;
+    constexpr int E = Fmt<BF16>::E;
+    const int full = V / E;                    // whole vectors of the row
+    auto whole = [&](int c) { return min(max(full - c * kCH, 0), kCH); };
+    const char *row = slot_row(P, slot);
+    const bool joins = wave == kWaves - 1;
+    float xt = 0.0f;
+    if (joins && tok >= 0) xt = logit_at<BF16>(row, tok);
+    u32x4 raw[kVPL];
+    if (wave < NC) issue_chunk<BF16>(raw, row, wave * kCH, whole(wave), V);
+    for (int c = wave; c < NC; c += kWaves) {
+        float x[kVPL][E];
+        widen<BF16>(raw, x, row, whole(c), V);
+        if (c + kWaves < NC) issue_chunk<BF16>(raw, row, (c + kWaves) * kCH, whole(c + kWaves), V);
+        float lm;
+        const float4 rec = chunk_record<E, ENT>(x, lm);
+        if (lane == 0) s_rec[c] = rec;
+        if (TOP) s_key[c][lane] = order_key(lm);
+    }
+    __syncthreads();
+    auto softmax = [&]() {
+        const Softmax f = join_records(s_rec, NC, s_rec[min(lane, NC - 1)]);
+        if (lane == 0) write_slot(P, slot, f, tok, xt);
+        return f;
+    };
+    if (TOP) top_of_slot<BF16>(P, sh, slot, row, [&](int c) { return s_key[c][lane]; }, softmax);
+    else if (joins) softmax();
 }
 
 // ---- gradient -------------------------------------------------------------------------------------
@@ -666,6 +735,19 @@ __global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(GradParams P
 }
 
 // ---- host -----------------------------------------------------------------------------------------
+// One kernel or two: a workgroup per slot while all of them are resident at once and the rows are short.
+// 231 slots of 20011 fp32: 12.7 us against 16.4; 128 of 1024: 8.2 against 10.3; but 16384 of 20011 337
+// against 337, 4096 of 1024 43 against 24, one of 126464 bf16 16 against 12 (the workgroup's compute unit is
+// then the limit).
+bool one_kernel(int64_t S, int64_t NC, int64_t cus) { return S <= 2 * cus && NC <= kShortRow; }
+
+constexpr int kChunksKernel = 0, kRowsKernel = 1;
+template <int K, bool BF16, bool ENT, bool TOP>
+constexpr auto kernel_of() {
+    if constexpr (K == kRowsKernel) return logprob_rows_kernel<BF16, ENT, TOP>;
+    else return logprob_chunks_kernel<BF16, ENT, TOP>;
+}
+
 // Records and lane maxima (with alternatives only) of a workspace, each part 256-byte aligned.
 bool workspace_of(int32_t rows, int32_t L, int32_t V, int32_t k, int32_t dtype, int &NV, int &NC, size_t &records,
                   size_t &total) {
@@ -743,30 +825,37 @@ extern "C" dllm_status dllm_logprobs(void *stream, const void *logits, int32_t d
     P.lane_max = (char *)workspace + records;
     P.status = status;
 
-    // The scoring kernel's grid rule: the same chunks per workgroup, the same measured thresholds.
     const hipStream_t st = (hipStream_t)stream;
     const int64_t S = (int64_t)rows * L, cus = cu_count(), boxed = S * P.NC;
-    int64_t grid = cus * (boxed < cus * kTinyBoxChunksPerCU ? 1 : boxed < cus * kSmallBoxChunksPerCU ? 2 : kGroupsPerCU);
-    grid = grid < (S + 2047) / 2048 ? (S + 2047) / 2048 : grid;
-    const int64_t most = (boxed + kWaves - 1) / kWaves;
-    grid = grid > most ? most : grid;
-    const int64_t per = (boxed + grid - 1) / grid;
-    const int win = (int)((per + P.NC - 1) / P.NC + 2);
-    const size_t lds = (size_t)win * sizeof(int);
-    const bool bf = dtype == DLLM_BF16, ent = entropy != nullptr;
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, st, P); };
-    if (bf) {
-        if (k > 0) ent ? go(logprob_chunks_kernel<true, true, true>) : go(logprob_chunks_kernel<true, false, true>);
-        else ent ? go(logprob_chunks_kernel<true, true, false>) : go(logprob_chunks_kernel<true, false, false>);
-    } else {
-        if (k > 0) ent ? go(logprob_chunks_kernel<false, true, true>) : go(logprob_chunks_kernel<false, false, true>);
-        else ent ? go(logprob_chunks_kernel<false, true, false>) : go(logprob_chunks_kernel<false, false, false>);
+    const bool bf = dtype == DLLM_BF16, ent = entropy != nullptr, top = k > 0;
+    auto pick = [&](auto go, auto kind) {
+        constexpr int K = decltype(kind)::value;
+        if (bf) {
+            if (top) ent ? go(kernel_of<K, true, true, true>()) : go(kernel_of<K, true, false, true>());
+            else ent ? go(kernel_of<K, true, true, false>()) : go(kernel_of<K, true, false, false>());
+        } else {
+            if (top) ent ? go(kernel_of<K, false, true, true>()) : go(kernel_of<K, false, false, true>());
+            else ent ? go(kernel_of<K, false, true, false>()) : go(kernel_of<K, false, false, false>());
+        }
+    };
+    if (one_kernel(S, P.NC, cus)) {
+        pick([&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)S), dim3(kThreads), 0, st, P); },
+             std::integral_constant<int, kRowsKernel>());
+        return check_hip(hipGetLastError(), "dllm_logprobs launch");
     }
+    // The scoring kernel's grid rule: the same chunks per workgroup, the same measured thresholds.
+    int64_t grid = cus * (boxed < cus * kTinyBoxChunksPerCU ? 1 : boxed < cus * kSmallBoxChunksPerCU ? 2 : kGroupsPerCU);
+    grid = std::max(grid, (S + 2047) / 2048);
+    grid = std::min(grid, (boxed + kWaves - 1) / kWaves);
+    const int64_t per = (boxed + grid - 1) / grid;
+    const size_t lds = (size_t)((per + P.NC - 1) / P.NC + 2) * sizeof(int);
+    pick([&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, st, P); },
+         std::integral_constant<int, kChunksKernel>());
     rc = check_hip(hipGetLastError(), "dllm_logprobs chunks launch");
     if (rc != DLLM_OK) return rc;
-    if (k > 0) {
-        if (bf) hipLaunchKernelGGL(logprob_top_kernel<true>, dim3((unsigned)S), dim3(kTopThreads), 0, st, P);
-        else hipLaunchKernelGGL(logprob_top_kernel<false>, dim3((unsigned)S), dim3(kTopThreads), 0, st, P);
+    if (top) {
+        if (bf) hipLaunchKernelGGL(logprob_top_kernel<true>, dim3((unsigned)S), dim3(64 * kJoinWaves), 0, st, P);
+        else hipLaunchKernelGGL(logprob_top_kernel<false>, dim3((unsigned)S), dim3(64 * kJoinWaves), 0, st, P);
         return check_hip(hipGetLastError(), "dllm_logprobs alternatives launch");
     }
     const dim3 jg((unsigned)((S + kJoinWaves - 1) / kJoinWaves)), jb(64 * kJoinWaves);
