@@ -418,8 +418,9 @@ __global__ __launch_bounds__(kSortWide) void sort_one_kernel(SortParams P) {
 
 // ---- sum and join ---------------------------------------------------------------------------------
 // Sorted tokens per piece: many where there is work for every compute unit, few where a wave's own chain of
-// loads is what takes the time (see launch).
-constexpr int kPiece = 64, kSmallPiece = 16;
+// loads is what takes the time: two batches of 1600 tokens of width 1000 take 51, 48, 46 us with 16, 12, 8; two of
+// 8192 of width 2048 take 116, 114, 123, and 147 with 64.
+constexpr int kPiece = 64, kSmallPiece = 12;
 constexpr int kSumThreads = 256;
 constexpr int kSumWaves = kSumThreads / 64;
 constexpr int kSumCols = 64 * kVec;            // columns per wave
@@ -448,9 +449,30 @@ __device__ __forceinline__ void write_row(const SumParams &P, int id, int v, con
     store8<TB>(P.table.p + id * P.table.stride_b, v, P.table.D, o);
 }
 
-// The window of three pieces around piece [N, 2N): ids, positions and run starts, spread over the lanes.
-template <int N>
-struct Window;
+// The window of three pieces around piece [N, 2N): ids, positions, run starts as bits (a position whose id
+// differs from the one before; the window's first counts) and counts of tokens with an id.
+template <int N>                               // up to 21 tokens: the window in one register, lanes 0 .. 3N-1
+struct Window {
+    int k, p;
+    __device__ __forceinline__ void load(const uint64_t *sorted, int64_t first, int n, uint64_t none) {
+        const int64_t i = first - N + lane_id();
+        const uint64_t w = i >= 0 && i < n && lane_id() < 3 * N ? sorted[i] : none;
+        k = (int)(w >> 32), p = (int)(uint32_t)w;
+    }
+    __device__ __forceinline__ void starts(uint64_t &s0, uint64_t &s1, uint64_t &s2) const {
+        constexpr uint64_t kPart = (1ull << N) - 1;
+        const int below = up_one(k);
+        const uint64_t s = __ballot(lane_id() == 0 || k != below);
+        s0 = s & kPart, s1 = (s >> N) & kPart, s2 = (s >> (2 * N)) & kPart;
+    }
+    __device__ __forceinline__ void counts(int none, int &c1, int &c2) const {
+        constexpr uint64_t kPart = (1ull << N) - 1;
+        const uint64_t on = __ballot(k != none);
+        c1 = __popcll((on >> N) & kPart), c2 = __popcll((on >> (2 * N)) & kPart);
+    }
+    __device__ __forceinline__ int key(int t) const { return __builtin_amdgcn_readlane(k, t); }
+    __device__ __forceinline__ int pos(int t) const { return __builtin_amdgcn_readlane(p, t); }
+};
 template <>
 struct Window<64> {
     int k0, k1, k2, p1, p2;
@@ -460,14 +482,13 @@ struct Window<64> {
                        w2 = i + 64 < n ? sorted[i + 64] : none;
         k0 = (int)(w0 >> 32), k1 = (int)(w1 >> 32), k2 = (int)(w2 >> 32), p1 = (int)(uint32_t)w1, p2 = (int)(uint32_t)w2;
     }
-    // bits of the positions whose id differs from the one before (the window's first position counts)
     __device__ __forceinline__ void starts(uint64_t &s0, uint64_t &s1, uint64_t &s2) const {
         const int lane = lane_id(), b0 = up_one(k0), b1 = up_one(k1), b2 = up_one(k2);
         s0 = __ballot(lane == 0 || k0 != b0);
         s1 = __ballot(k1 != (lane == 0 ? __builtin_amdgcn_readlane(k0, 63) : b1));
         s2 = __ballot(k2 != (lane == 0 ? __builtin_amdgcn_readlane(k1, 63) : b2));
     }
-    __device__ __forceinline__ void counts(int none, int &c1, int &c2) const {   // tokens with an id
+    __device__ __forceinline__ void counts(int none, int &c1, int &c2) const {
         c1 = __popcll(__ballot(k1 != none));
         c2 = __popcll(__ballot(k2 != none));
     }
@@ -478,27 +499,6 @@ struct Window<64> {
         return t < 128 ? __builtin_amdgcn_readlane(p1, t - 64) : __builtin_amdgcn_readlane(p2, t - 128);
     }
 };
-template <>
-struct Window<16> {
-    int k, p;                                  // lanes 0 .. 47
-    __device__ __forceinline__ void load(const uint64_t *sorted, int64_t first, int n, uint64_t none) {
-        const int64_t i = first - 16 + lane_id();
-        const uint64_t w = i >= 0 && i < n && lane_id() < 48 ? sorted[i] : none;
-        k = (int)(w >> 32), p = (int)(uint32_t)w;
-    }
-    __device__ __forceinline__ void starts(uint64_t &s0, uint64_t &s1, uint64_t &s2) const {
-        const int below = up_one(k);
-        const uint64_t s = __ballot(lane_id() == 0 || k != below);
-        s0 = s & 0xFFFF, s1 = (s >> 16) & 0xFFFF, s2 = (s >> 32) & 0xFFFF;
-    }
-    __device__ __forceinline__ void counts(int none, int &c1, int &c2) const {
-        const uint64_t on = __ballot(k != none);
-        c1 = __popcll((on >> 16) & 0xFFFF), c2 = __popcll((on >> 32) & 0xFFFF);
-    }
-    __device__ __forceinline__ int key(int t) const { return __builtin_amdgcn_readlane(k, t); }
-    __device__ __forceinline__ int pos(int t) const { return __builtin_amdgcn_readlane(p, t); }
-};
-
 // One wave: piece `piece`, columns colblock*512 ...
 template <bool GB, bool TB, int N, bool OLD>
 __device__ void sum_piece(const SumParams &P, int piece, int colblock) {
@@ -682,7 +682,8 @@ GradSpace grad_space(int64_t n, int64_t D) {
     while ((n + w.tile - 1) / w.tile > kMaxTiles) w.tile *= 2;
     w.tiles = (int)((n + w.tile - 1) / w.tile);
     // Fewer than kSmallUnits waves at kPiece tokens leave compute units idle while each wave works through
-    // its tokens: shorter pieces then.
+    // its tokens: shorter pieces then (a limit of 512 costs 16384 tokens of width 1024 10 us, one of 8192
+    // costs 163840 of width 64 20 us).
     const int64_t units = (n + kPiece - 1) / kPiece * ((D + kSumCols - 1) / kSumCols);
     w.piece = units < kSmallUnits ? kSmallPiece : kPiece;
     w.pieces = (int)((n + w.piece - 1) / w.piece);

@@ -1,8 +1,8 @@
 """dllm_embed and dllm_embed_grad on the GPU against the float64 oracle.
 
 Tolerances: the lookup is one float32 product rounded once more to the output's type, u |ref| + half a
-step.  The gradient sums c terms in float32 in chains: at most min(c, 64 + c/1024 + 17) additions deep
-(64 tokens of a piece, a slice's pieces, 16 slices), each off by u of the sum of absolute terms, then
+step.  The gradient sums c terms in float32 in chains: at most min(c, 64 + c/192 + 17) additions deep
+(up to 64 tokens of a piece, a sixteenth of the pieces of at least 12 tokens, 16 slices), each off by u of the sum of absolute terms, then
 one FMA with the scale (and the row it adds to) and half a step of the type.
 """
 import numpy as np
@@ -112,10 +112,9 @@ def _ids(kind, n, V, rng):
         a = rng.integers(0, V, n)
         a[rng.random(n) < 0.5] = V // 2
         return a
-    if kind == "runs-of-64":                   # every id exactly as long as a piece
-        return rng.permutation(np.repeat(np.arange((n + 63) // 64) % V, 64)[:n])
-    if kind == "runs-of-65":
-        return rng.permutation(np.repeat(np.arange((n + 64) // 65) % V, 65)[:n])
+    if kind.startswith("runs-of-"):            # every id as long as a piece, or one token longer
+        m = int(kind.split("-")[-1])
+        return rng.permutation(np.repeat(np.arange((n + m - 1) // m) % V, m)[:n])
     if kind == "ascending":
         return np.arange(n) % V
     if kind == "descending":
@@ -124,7 +123,7 @@ def _ids(kind, n, V, rng):
 
 
 def check_grad(got, ref, size, count, dtype, base=None):
-    depth = np.minimum(count, 64 + count // 1024 + 17)[:, None]
+    depth = np.minimum(count, 64 + count // 192 + 17)[:, None]
     tol = U * (depth + 2) * size
     total = ref if base is None else ref + base
     tol = tol + HALF[dtype] * (np.abs(total) + tol) + 2 * U * np.abs(total)
@@ -142,7 +141,10 @@ def check_grad(got, ref, size, count, dtype, base=None):
     (9000, 3, 40, "spread", "bf16", "fp32", 0, 0), (20000, 152066, 72, "half-mask", "bf16", "bf16", 0, 0),
     (70001, 9, 16, "half-mask", "fp32", "fp32", 0, 0), (5000, 300000, 16, "half-mask", "bf16", "fp32", 0, 0),
     (33, 70, 2056, "spread", "bf16", "bf16", 0, 0), (300, 7, 4100, "half-mask", "bf16", "bf16", 0, 0),
-    (150000, 50000, 8, "spread", "bf16", "fp32", 0, 0)])
+    (150000, 50000, 8, "spread", "bf16", "fp32", 0, 0), (150000, 70, 8, "half-mask", "fp32", "fp32", 0, 0),
+    (131200, 2100, 8, "runs-of-64", "bf16", "bf16", 0, 0), (133250, 2100, 8, "runs-of-65", "fp32", "bf16", 0, 1),
+    (132000, 1, 8, "one", "fp32", "fp32", 0, 0), (600, 60, 24, "runs-of-12", "fp32", "fp32", 0, 0),
+    (650, 60, 24, "runs-of-13", "bf16", "fp32", 0, 0)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_gradient(n, V, D, kind, go, table, extra, offset, accumulate):
     from confidence_block_unmasking_amd import api
@@ -165,6 +167,30 @@ def test_gradient(n, V, D, kind, go, table, extra, offset, accumulate):
     assert np.array_equal(got[absent], base[absent]) if accumulate else not got[absent].any()
     if extra:
         assert (t.as_strided((V, extra), (D + extra, 1), t.storage_offset() + D) == 776.0).all()
+
+
+@pytest.mark.parametrize("n", [3000, 9000])
+def test_gradient_of_a_large_table(n):
+    """A table whose zeros hide the sort (from 768 MiB on): every row that occurs against float64 sums of its
+    tokens, every other row zero, the columns past D untouched."""
+    from confidence_block_unmasking_amd import api
+    rng = np.random.default_rng(n)
+    V, D, pitch = 210000, 2001, 2004
+    buf = torch.full((V, pitch), 776.0, dtype=torch.bfloat16, device="cuda")
+    t = buf[:, :D]
+    ids = torch.from_numpy(_ids("half-mask", n, V, rng).astype(np.int32)).cuda()
+    g = torch.randn((n, D), device="cuda").to(torch.bfloat16)
+    st = _status()
+    api.dllm_embed_grad(g, ids, t, api.new_embed_grad_workspace(n, V, D), st, scale=0.5)
+    names, back = ids.long().unique(return_inverse=True)
+    ref = torch.zeros((names.numel(), D), dtype=torch.float64, device="cuda").index_add_(0, back, 0.5 * g.double())
+    size = torch.zeros_like(ref).index_add_(0, back, 0.5 * g.double().abs())
+    depth = torch.bincount(back).clamp(max=81 + n // 192)[:, None]
+    tol = U * (depth + 2) * size
+    assert ((t[names].double() - ref).abs() <= tol + HALF["bf16"] * (ref.abs() + tol)).all()
+    absent = torch.ones(V, dtype=torch.bool, device="cuda")
+    absent[names] = False
+    assert not t[absent].any() and (buf[:, D:] == 776.0).all() and int(st.item()) == 0
 
 
 def test_gradient_without_tokens():
@@ -260,3 +286,26 @@ def test_replays_of_a_captured_graph_and_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(a["out"], b["out"]) and torch.equal(a["grad"], b["grad"]), seed
     assert int(st.item()) == 0
+
+
+def test_binding_refuses_what_the_kernels_cannot_read():
+    from confidence_block_unmasking_amd import api
+    t, ids, out, st = torch.zeros((9, 16), device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda"), torch.zeros(
+        (5, 16), device="cuda"), _status()
+    ws = api.new_embed_grad_workspace(5, 9, 16)
+    for kw in (dict(table=t.half()), dict(table=t.cpu()), dict(table=t.t()), dict(ids=ids.long()), dict(ids=ids[::2]),
+               dict(out=out[:4]), dict(out=out[:, :8]), dict(out=out.t()), dict(valid=torch.ones(4, dtype=torch.uint8, device="cuda")),
+               dict(valid=torch.ones(5, dtype=torch.bool, device="cuda")), dict(status=st.float())):
+        with pytest.raises(ValueError):
+            api.dllm_embed(**{**dict(table=t, ids=ids, out=out, status=st), **kw})
+    with pytest.raises(api.DllmError):
+        api.dllm_embed(t, ids, t[4:], st)          # out overlaps the table
+    good = dict(grad_out=out, ids=ids, grad_table=t, workspace=ws, status=st)
+    for kw in (dict(grad_out=out[:4]), dict(grad_out=out[:, :8]), dict(grad_table=t.double()), dict(ids=ids.float()),
+               dict(workspace=ws.float())):
+        with pytest.raises(ValueError):
+            api.dllm_embed_grad(**{**good, **kw})
+    for kw in (dict(workspace=ws[:64]), dict(workspace=ws[16:]), dict(grad_table=t[:1].expand(9, 16))):
+        with pytest.raises(api.DllmError):
+            api.dllm_embed_grad(**{**good, **kw})
+    torch.cuda.synchronize()

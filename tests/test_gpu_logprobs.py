@@ -265,6 +265,10 @@ def test_bits_depend_on_the_slot_alone():
     one, _ = run(buf, rows, L, V, ps, 0, mask, tokens, 20)
     for n in full:
         assert np.array_equal(full[n][17, 3].view(np.uint32), one[n][17, 3].view(np.uint32)), n
+    # a box of one row is finished by one kernel, the box of 768 slots by two
+    row, _ = run(buf[17 * L * V:], 1, L, V, ps, 0, np.ones((1, L), bool), tokens[17:18], 20)
+    for n in full:
+        assert np.array_equal(full[n][17].view(np.uint32), row[n][0].view(np.uint32)), n
 
 
 def test_offsets_past_32_bits():
@@ -475,3 +479,65 @@ def test_replays_of_a_captured_graph_and_another_stream():
         for n in ("lp", "ent", "sta", "ti", "tl", "grad"):
             assert torch.equal(a[n], b[n]), (seed, n)
     assert int(st.item()) == 0
+
+
+def test_binding_refuses_what_the_kernels_cannot_read():
+    from confidence_block_unmasking_amd import api
+    f = dict(dtype=torch.float32, device="cuda")
+    lg, mask = torch.zeros((2, 4, 50), **f), torch.ones((2, 4), dtype=torch.uint8, device="cuda")
+    tok, out = torch.zeros((2, 4), dtype=torch.int32, device="cuda"), torch.zeros((2, 4), **f)
+    ws, st = api.new_logprobs_workspace(2, 4, 50, 3, torch.float32), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ids, tl = torch.zeros((2, 4, 3), dtype=torch.int32, device="cuda"), torch.zeros((2, 4, 3), **f)
+    sta, grad = torch.zeros((2, 4, 2), **f), torch.zeros((2, 4, 50), **f)
+    bad = [dict(tokens=tok.long()), dict(tokens=tok.t()), dict(tokens=tok[:, :3]), dict(tokens=tok.cpu()),
+           dict(logprob=out[:1]), dict(logprob=out.double()), dict(mask=mask.bool()), dict(mask=mask[:1]),
+           dict(logits=lg.half()), dict(logits=lg.transpose(1, 2)), dict(entropy=out.t()), dict(stats=out),
+           dict(top_ids=ids.long()), dict(top_ids=ids, top_logprobs=tl[:1]), dict(exclude=mask[:1]), dict(status=st.long()),
+           dict(logits=lg.cpu()), dict(V=60), dict(k=4, top_ids=ids, top_logprobs=tl)]
+    for kw in bad:
+        a = dict(logits=lg, mask=mask, tokens=tok, logprob=out, workspace=ws, status=st)
+        if "V" in kw:
+            a.update(rows=2, L=4, V=60, pos_stride=60, row_stride=240)
+            kw = {}
+        with pytest.raises(ValueError):
+            api.dllm_logprobs(**{**a, **kw})
+    for kw in (dict(top_ids=ids), dict(workspace=ws[:16]), dict(logprob=None)):
+        with pytest.raises(api.DllmError):
+            api.dllm_logprobs(**{**dict(logits=lg, mask=mask, tokens=tok, logprob=out, workspace=ws, status=st), **kw})
+    good = dict(logits=lg, mask=mask, tokens=tok, stats=sta, grad_logprob=out, grad_logits=grad, status=st)
+    for kw in (dict(grad_logits=grad.bfloat16()), dict(grad_logits=grad[:, :, :40]), dict(stats=out), dict(grad_logprob=out[:1]),
+               dict(grad_entropy=out.double()), dict(grad_logits=grad.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            api.dllm_logprobs_grad(**{**good, **kw})
+    for kw in (dict(grad_entropy=out), dict(grad_logprob=None), dict(grad_logits=lg.view(-1)[1:], rows=1, L=4, V=49,
+                                                                       pos_stride=49, row_stride=196)):
+        with pytest.raises(api.DllmError):
+            api.dllm_logprobs_grad(**{**good, **kw})
+    torch.cuda.synchronize()
+
+
+def test_calls_on_two_streams_at_once():
+    """Two boxes scored at the same time on two streams, each with its own workspace."""
+    rng = np.random.default_rng(21)
+    V, k = 20011, 7
+    from confidence_block_unmasking_amd import api
+    boxes = []
+    for rows, L in ((40, 32), (3, 16)):
+        buf, x, ps = make_logits(rng, rows, L, V, "bf16")
+        f = dict(dtype=torch.float32, device="cuda")
+        boxes.append(dict(buf=buf, x=x, rows=rows, L=L, s=torch.cuda.Stream(),
+                          tok=torch.from_numpy(rng.integers(0, V, (rows, L)).astype(np.int32)).cuda(),
+                          mask=torch.ones((rows, L), dtype=torch.uint8, device="cuda"), lp=torch.zeros((rows, L), **f),
+                          ti=torch.zeros((rows, L, k), dtype=torch.int32, device="cuda"), tl=torch.zeros((rows, L, k), **f),
+                          ws=api.new_logprobs_workspace(rows, L, V, k), st=torch.zeros(1, dtype=torch.int32, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for b in boxes:
+            api.dllm_logprobs(b["buf"], b["mask"], b["tok"], b["lp"], b["ws"], b["st"], top_ids=b["ti"], top_logprobs=b["tl"],
+                              rows=b["rows"], L=b["L"], V=V, pos_stride=V, row_stride=b["L"] * V, stream=b["s"])
+    torch.cuda.synchronize()
+    for b in boxes:
+        for r, j in ((0, 0), (b["rows"] - 1, b["L"] - 1)):
+            o = olp.slot(b["x"][r, j], token=int(b["tok"][r, j].item()), k=k)
+            assert np.array_equal(b["ti"][r, j].cpu().numpy(), o["top_ids"])
+            assert abs(b["lp"][r, j].item() - o["logprob"]) <= tol_logprob(o, V, o["logprob"])
