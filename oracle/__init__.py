@@ -12,6 +12,8 @@ by eye, with no blocking, fusion or reordering:
   compact.py  block-boundary scatter, advance/evict, token-budget admission, row layout
   loop.py     synchronous and first-done-first-out loops, idle request-step accounting
   rows.py     the per-slot confidence/argmax of step.py in C (rows.c), for replaying whole loops
+  logprobs.py, embed.py             the two sides of the forward: token log probabilities, entropy and
+              alternatives, embedding lookup, and their gradients
   quota.py, shard.py, features.py   the next rows: fixed per-step quota, vocabulary shards,
               step-predictor features
 
