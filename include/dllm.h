@@ -380,7 +380,8 @@ dllm_status dllm_compact(void *stream, int32_t rows, int32_t L, int32_t W, int32
  * Errors: those of dllm_step for logits, shape, strides and workspace, and DLLM_ERR_SHAPE for V > 2^30;
  * DLLM_ERR_ARG for k out of
  * range, token_stride < L, logits not aligned to their type, tokens without logprob or the reverse,
- * k > 0 without its outputs, or nothing to compute.  rows == 0 is a no-op.  Work: two kernels. */
+ * k > 0 without its outputs, or nothing to compute.  rows == 0 is a no-op.  Work: one kernel for few
+ * short rows, otherwise two. */
 size_t dllm_logprobs_workspace_bytes(int32_t rows, int32_t L, int32_t V, int32_t k, int32_t dtype);
 dllm_status dllm_logprobs(void *stream, const void *logits, int32_t dtype, int64_t pos_stride,
                           int64_t row_stride, int32_t rows, int32_t L, int32_t V, const uint8_t *mask,
