@@ -8,7 +8,9 @@
 //
 // Lookup (gfx950): a gather bound by HBM writes (and reads of the distinct rows).  A wave takes one token
 // and 2048 of its columns (kLookVecs vectors of 8 elements per lane, all in flight together); narrow
-// tables put several tokens side by side in a wave.
+// tables put several tokens side by side in a wave.  128 x 1280 tokens of width 4096, bf16 (0.33 GB of rows
+// read, 1.34 GB written) take 305 us = 5.5 TB/s; 1, 2, 3, 8 vectors per lane take 424, 322, 314, 323, four tokens
+// per thread 389, non-temporal row reads 378 (hot rows live in the caches), plain stores 366.
 //
 // Gradient: the tokens are sorted by id (stable, so a row's terms are summed in token order and the
 // bits never depend on timing; no float atomics), then every run of equal ids is summed once and
@@ -26,6 +28,9 @@
 //      end, so runs up to kPiece tokens are never split.  A longer run (the mask token of a training
 //      box can hold half of all tokens) leaves one partial sum per piece it covers.
 //   3. Join: the partial sums of each long run, in order.
+// 64 x 544 tokens of width 4096 into 152066 bf16 rows take 288 us, of which the zeros (1.25 GB) 202 with the sort
+// behind them, the sums 75 (0.32 GB, while the last-level cache still drains zeros; 75 for 0.41 GB when
+// accumulating), the join 8.  Two batches of 1600 tokens of width 1000 take 49 us, bound by six dependent launches.
 #include <algorithm>
 #include <type_traits>
 
@@ -425,7 +430,7 @@ constexpr int kSumThreads = 256;
 constexpr int kSumWaves = kSumThreads / 64;
 constexpr int kSumCols = 64 * kVec;            // columns per wave
 // Tokens whose loads are in flight together; with the table's old rows beside them, half as many.
-constexpr int kAhead = 8, kAheadOld = 4;
+constexpr int kAhead = 8, kAheadOld = 4;      // 2 to 16 make no difference at 64 x 544 tokens (HBM-bound)
 
 struct SumParams {
     const char *grad;

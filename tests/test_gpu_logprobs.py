@@ -93,6 +93,8 @@ def check(g, x, on, tokens, k, where=""):
                 continue
             o = olp.slot(x[r, j], token=tokens[r, j], k=k)
             at = f"{where} slot {r},{j}"
+            assert g["logprob"][r, j] <= 0 and (g["entropy"] is None or g["entropy"][r, j] >= 0), at
+            assert g["top_logprobs"] is None or (g["top_logprobs"][r, j] <= 0).all(), at
             if np.isneginf(o["logprob"]) or o["logprob"] < -FMAX:
                 assert np.isneginf(g["logprob"][r, j]), at
             else:
@@ -219,7 +221,7 @@ def test_special_rows(V, dtype):
         check(sub, xr[:, i:i + 1], np.ones((1, 1), bool), tokens[:, i:i + 1], k, s)
 
 
-@pytest.mark.parametrize("V,dtype", [(100, "fp32"), (9001, "bf16")])
+@pytest.mark.parametrize("V,dtype", [(100, "fp32"), (9001, "bf16"), (100001, "bf16"), (70000, "fp32")])
 def test_slots_without_a_distribution_read_nan(V, dtype):
     rng = np.random.default_rng(1)
     x = rng.normal(size=(1, 4, V)).astype(np.float32)
@@ -237,17 +239,20 @@ def test_slots_without_a_distribution_read_nan(V, dtype):
     check(one, xr[:, 3:], np.ones((1, 1), bool), tokens[:, 3:], 5)
 
 
-def test_tokens_out_of_range_report_and_read_nan():
+@pytest.mark.parametrize("V,k", [(300, 2), (140000, 2), (140000, 0)])
+def test_tokens_out_of_range_report_and_read_nan(V, k):
     rng = np.random.default_rng(2)
-    buf, x, ps = make_logits(rng, 1, 4, 300, "fp32")
-    tokens = np.array([[-1, 300, 7, 1 << 30]])
-    g, st = run(buf, 1, 4, 300, ps, 0, np.ones((1, 4), bool), tokens, 2)
+    buf, x, ps = make_logits(rng, 1, 4, V, "fp32")
+    tokens = np.array([[-1, V, 7, 1 << 30]])
+    g, st = run(buf, 1, 4, V, ps, 0, np.ones((1, 4), bool), tokens, k)
     assert st == 1
     assert np.isnan(g["logprob"][0, [0, 1, 3]]).all()
     o = olp.slot(x[0, 2], token=7)
-    assert abs(g["logprob"][0, 2] - o["logprob"]) <= tol_logprob(o, 300, o["logprob"])
+    assert abs(g["logprob"][0, 2] - o["logprob"]) <= tol_logprob(o, V, o["logprob"])
     for j in range(4):                          # everything else is unaffected
-        assert np.array_equal(g["top_ids"][0, j], olp.slot(x[0, j], k=2)["top_ids"])
+        o = olp.slot(x[0, j], k=k)
+        assert abs(g["entropy"][0, j] - o["entropy"]) <= tol_entropy(o, V)
+        assert k == 0 or np.array_equal(g["top_ids"][0, j], o["top_ids"])
 
 
 def test_bits_depend_on_the_slot_alone():
