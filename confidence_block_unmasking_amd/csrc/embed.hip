@@ -44,30 +44,54 @@ constexpr int kVec = 8;                        // elements per vector
 constexpr int kLookWaves = 2;                  // waves per workgroup of the lookup
 constexpr int kLookVecs = 4;                   // vectors per lane
 
-// Elements [v*8, v*8 + 8) of a row of D: as stored, to keep several in flight, and widened.  Only a row's
-// ragged end is read element by element.
+// A lane's 8 columns: c .. c+7, or (SPLIT) c .. c+3 and c+half .. c+half+3.  8 neighbours are 16 bytes of bf16; of
+// fp32 they are two stores that each cover half of every 32 bytes, where two groups of 4 are two dense ones: 292 us
+// against 446 for 163840 rows of 2048 looked up from bf16 into fp32, 339 against 406 from fp32.  (The gradient's
+// sums gain nothing from it: they are bound elsewhere, and bf16 loads of 8 bytes cost its small case 10 us of 48.)
+template <bool BF16>
+struct Group {
+    typedef uint32_t vec __attribute__((ext_vector_type(BF16 ? 2 : 4)));
+    typedef vec any __attribute__((aligned(BF16 ? 2 : 4)));
+};
+// 4 columns as stored (0 past D), the row's ragged end element by element.
+template <bool BF16>
+__device__ __forceinline__ typename Group<BF16>::vec load_group(const char *row, int c, int D) {
+    typedef typename Group<BF16>::any any;
+    if (c + 4 <= D) return *(const any *)(row + (int64_t)c * (BF16 ? 2 : 4));
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        w[e] = c + e >= D ? 0u : BF16 ? (uint32_t)((const uint16_t *)row)[c + e] : ((const uint32_t *)row)[c + e];
+    typename Group<BF16>::vec r;
+    if constexpr (BF16) r = {w[0] | w[1] << 16, w[2] | w[3] << 16};
+    else r = {w[0], w[1], w[2], w[3]};
+    return r;
+}
 template <bool BF16>
 struct Raw {
     u32x4 a[BF16 ? 1 : 2];
 };
-template <bool BF16>
-__device__ __forceinline__ Raw<BF16> load_raw(const char *row, int v, int D) {
+template <bool BF16, bool SPLIT>
+__device__ __forceinline__ Raw<BF16> load_raw(const char *row, int c, int half, int D) {
     typedef typename Row<BF16>::vec vec;
     Raw<BF16> r;
-    if ((v + 1) * kVec <= D) {
-        if (BF16) {
-            r.a[0] = ((const vec *)row)[v];
+    if constexpr (SPLIT) {
+        const auto lo = load_group<BF16>(row, c, D), hi = load_group<BF16>(row, c + half, D);
+        if constexpr (BF16) {
+            r.a[0] = u32x4{lo.x, lo.y, hi.x, hi.y};
         } else {
-            r.a[0] = ((const vec *)row)[2 * v];
-            r.a[BF16 ? 0 : 1] = ((const vec *)row)[2 * v + 1];
+            r.a[0] = lo;
+            r.a[1] = hi;
         }
+    } else if (c + 8 <= D) {
+        const vec *at = (const vec *)(row + (int64_t)c * (BF16 ? 2 : 4));
+        r.a[0] = at[0];
+        if (!BF16) r.a[BF16 ? 0 : 1] = at[1];
     } else {
         uint32_t w[kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const int d = v * kVec + e;
-            w[e] = d >= D ? 0u : BF16 ? (uint32_t)((const uint16_t *)row)[d] : ((const uint32_t *)row)[d];
-        }
+        for (int e = 0; e < kVec; ++e)
+            w[e] = c + e >= D ? 0u : BF16 ? (uint32_t)((const uint16_t *)row)[c + e] : ((const uint32_t *)row)[c + e];
         if (BF16) {
             r.a[0] = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
         } else {
@@ -82,28 +106,50 @@ __device__ __forceinline__ void widen(const Raw<BF16> &r, float (&x)[kVec]) {
     unpack<BF16>(r.a[0], x);
     if (!BF16) unpack<BF16>(r.a[BF16 ? 0 : 1], x + 4);
 }
-
 template <bool BF16>
-__device__ __forceinline__ void store8(char *row, int v, int D, const float (&x)[kVec]) {
+__device__ __forceinline__ void store_group(char *row, int c, int D, const float *x) {
+    typedef typename Group<BF16>::any any;
+    if (c + 4 <= D) {
+        typename Group<BF16>::vec v;
+        if constexpr (BF16) v = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+        else v = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+        __builtin_nontemporal_store(v, (any *)(row + (int64_t)c * (BF16 ? 2 : 4)));
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (c + e < D) {
+            if (BF16) ((uint16_t *)row)[c + e] = (uint16_t)pack_bf16(x[e], 0.0f);
+            else ((float *)row)[c + e] = x[e];
+        }
+    }
+}
+template <bool BF16, bool SPLIT>
+__device__ __forceinline__ void store8(char *row, int c, int half, int D, const float (&x)[kVec]) {
     typedef typename Row<BF16>::vec vec;
-    if ((v + 1) * kVec <= D) {
+    if (!SPLIT && c + 8 <= D) {
+        vec *at = (vec *)(row + (int64_t)c * (BF16 ? 2 : 4));
         if (BF16) {
             const u32x4 a = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-            __builtin_nontemporal_store(a, (vec *)row + v);
+            __builtin_nontemporal_store(a, at);
         } else {
             const u32x4 a = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
             const u32x4 b = {__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])};
-            __builtin_nontemporal_store(a, (vec *)row + 2 * v);
-            __builtin_nontemporal_store(b, (vec *)row + 2 * v + 1);
+            __builtin_nontemporal_store(a, at);
+            __builtin_nontemporal_store(b, at + 1);
         }
-    } else {
+        return;
+    }
+    if (SPLIT) {
+        store_group<BF16>(row, c, D, x);
+        store_group<BF16>(row, c + half, D, x + 4);
+        return;
+    }
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const int d = v * kVec + e;
-            if (d < D) {
-                if (BF16) ((uint16_t *)row)[d] = (uint16_t)pack_bf16(x[e], 0.0f);
-                else ((float *)row)[d] = x[e];
-            }
+    for (int e = 0; e < kVec; ++e) {
+        if (c + e < D) {
+            if (BF16) ((uint16_t *)row)[c + e] = (uint16_t)pack_bf16(x[e], 0.0f);
+            else ((float *)row)[c + e] = x[e];
         }
     }
 }
@@ -115,7 +161,7 @@ struct EmbedParams {
     int64_t out_stride_b;
     const int32_t *ids;
     const uint8_t *valid;
-    int32_t n, n_vocab, D, nv;                 // nv: vectors of a row
+    int32_t n, n_vocab, D;
     int32_t lanes_log2, segs;                  // lanes per token (a power of two); waves per token when that is 64
     float scale;
     int32_t *status;
@@ -124,17 +170,19 @@ struct EmbedParams {
 // WIDE: a whole wave per token, so the token and its id are wave-uniform (scalar loads).
 template <bool TB, bool OB, bool WIDE>
 __global__ __launch_bounds__(64 * kLookWaves) void embed_kernel(EmbedParams P) {
-    fetch_args(P.table, P.table_stride_b, P.out, P.out_stride_b, P.ids, P.valid, P.n, P.n_vocab, P.D, P.nv, P.scale);
+    fetch_args(P.table, P.table_stride_b, P.out, P.out_stride_b, P.ids, P.valid, P.n, P.n_vocab, P.D, P.scale);
+    constexpr bool SPLIT = !OB;
     const uint32_t unit = blockIdx.x * kLookWaves + uni(threadIdx.x >> 6);
     const int lane = lane_id(), step = WIDE ? 64 : 1 << P.lanes_log2;
+    const int half = SPLIT ? step * 4 : 4;
     uint32_t t;
-    int v0;
+    int c0 = 0, lv = lane;                     // first column of the wave's part of the token; lane within it
     if (WIDE) {
         t = unit / P.segs;
-        v0 = (unit - t * P.segs) * (64 * kLookVecs) + lane;
+        c0 = (unit - t * P.segs) * (64 * kLookVecs * kVec);
     } else {
         t = (unit << (6 - P.lanes_log2)) + (lane >> P.lanes_log2);
-        v0 = lane & (step - 1);
+        lv = lane & (step - 1);
     }
     if (t >= (uint32_t)P.n) return;
     int id = P.ids[t];                         // the row to read, -1 for zeros
@@ -145,21 +193,22 @@ __global__ __launch_bounds__(64 * kLookWaves) void embed_kernel(EmbedParams P) {
     }
     const char *row = P.table + id * P.table_stride_b;
     char *out = P.out + t * P.out_stride_b;
+    c0 += lv * (SPLIT ? 4 : kVec);
     Raw<TB> raw[kLookVecs];
 #pragma unroll
     for (int i = 0; i < kLookVecs; ++i) {
-        const int v = v0 + i * step;
-        if (id >= 0 && v < P.nv) raw[i] = load_raw<TB>(row, v, P.D);
+        const int c = c0 + i * step * kVec;
+        if (id >= 0 && c < P.D) raw[i] = load_raw<TB, SPLIT>(row, c, half, P.D);
     }
 #pragma unroll
     for (int i = 0; i < kLookVecs; ++i) {
-        const int v = v0 + i * step;
-        if (v >= P.nv) continue;
+        const int c = c0 + i * step * kVec;
+        if (c >= P.D) continue;
         float x[kVec];
         widen<TB>(raw[i], x);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) x[e] = id >= 0 ? x[e] * P.scale : 0.0f;
-        store8<OB>(out, v, P.D, x);
+        store8<OB, SPLIT>(out, c, half, P.D, x);
     }
 }
 
@@ -167,7 +216,7 @@ __global__ __launch_bounds__(64 * kLookWaves) void embed_kernel(EmbedParams P) {
 struct Table {
     char *p;
     int64_t stride_b;
-    int32_t n_vocab, D, nv;                    // nv: 8-element vectors of a row
+    int32_t n_vocab, D;
     int32_t fill, fill_log2;                   // 16-byte vectors of a row (a ragged one too), also as a power of two not below it
 };
 
@@ -447,11 +496,11 @@ __device__ __forceinline__ int key_of(uint64_t item) { return (int)(item >> 32);
 
 // table row = (old +) scale * sum, rounded once.
 template <bool TB>
-__device__ __forceinline__ void write_row(const SumParams &P, int id, int v, const float (&a)[kVec], const float (&old)[kVec]) {
+__device__ __forceinline__ void write_row(const SumParams &P, int id, int c, const float (&a)[kVec], const float (&old)[kVec]) {
     float o[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) o[e] = fmaf(P.scale, a[e], old[e]);
-    store8<TB>(P.table.p + id * P.table.stride_b, v, P.table.D, o);
+    store8<TB, false>(P.table.p + id * P.table.stride_b, c, 4, P.table.D, o);
 }
 
 // The window of three pieces around piece [N, 2N): ids, positions, run starts as bits (a position whose id
@@ -552,8 +601,9 @@ __device__ void sum_piece(const SumParams &P, int piece, int colblock) {
     if (tail < 3 * N && colblock == 0 && lane_id() == 0) P.long_piece[atomicAdd(P.n_long, 1)] = piece;
 
     // lanes past the last column keep running (their registers are read across the wave) on its vector
-    const int own = colblock * 64 + lane_id(), v = min(own, P.table.nv - 1);
-    const bool live = own < P.table.nv;
+    const int own = colblock * kSumCols + lane_id() * kVec;
+    const bool live = own < D;
+    const int c = min(own, (D - 1) / kVec * kVec);
     auto ends_run = [&](int t) { return t + 1 == end || next_start(t + 1) == t + 1; };
     auto to_row = [&](int t) { return t + 1 != head_end && t < tail; };
     float a[kVec];
@@ -566,8 +616,8 @@ __device__ void sum_piece(const SumParams &P, int piece, int colblock) {
         for (int u = 0; u < kStep; ++u) {
             const int t = t0 + u;
             if (t < end) {
-                raw[u] = load_raw<GB>(P.grad + w.pos(t) * P.grad_stride_b, v, D);
-                if (OLD && ends_run(t) && to_row(t)) old[u] = load_raw<TB>(P.table.p + w.key(t) * P.table.stride_b, v, D);
+                raw[u] = load_raw<GB, false>(P.grad + w.pos(t) * P.grad_stride_b, c, 4, D);
+                if (OLD && ends_run(t) && to_row(t)) old[u] = load_raw<TB, false>(P.table.p + w.key(t) * P.table.stride_b, c, 4, D);
             }
         }
 #pragma unroll
@@ -585,12 +635,12 @@ __device__ void sum_piece(const SumParams &P, int piece, int colblock) {
                 for (int e = 0; e < kVec; ++e) o[e] = 0.0f;
                 if (OLD) widen<TB>(old[u], o);
                 const int id = w.key(t);
-                if (live) write_row<TB>(P, id, v, a, o);
+                if (live) write_row<TB>(P, id, c, a, o);
             } else {
                 float *part = P.part + ((int64_t)piece * 2 + (t + 1 == head_end ? 0 : 1)) * D;
 #pragma unroll
                 for (int e = 0; e < kVec; ++e)
-                    if (live && v * kVec + e < D) part[v * kVec + e] = a[e];
+                    if (live && c + e < D) part[c + e] = a[e];
             }
 #pragma unroll
             for (int e = 0; e < kVec; ++e) a[e] = 0.0f;
@@ -650,19 +700,19 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams P) {
         for (int e = 0; e < 4; ++e) s_sum[slice][c + e] = a[e];
         __syncthreads();
         if (tid < kJoinCols / kVec) {
-            const int v = blockIdx.x * (kJoinCols / kVec) + tid;
+            const int c8 = blockIdx.x * kJoinCols + tid * kVec;
             float t[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 t[e] = 0.0f;
                 for (int s = 0; s < kJoinSlices; ++s) t[e] += s_sum[s][tid * kVec + e];
             }
-            if (v * kVec < D) {
+            if (c8 < D) {
                 float o[kVec];
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) o[e] = 0.0f;
-                if (P.accumulate) widen<TB>(load_raw<TB>(P.table.p + key * P.table.stride_b, v, D), o);
-                write_row<TB>(P, key, v, t, o);
+                if (P.accumulate) widen<TB>(load_raw<TB, false>(P.table.p + key * P.table.stride_b, c8, 4, D), o);
+                write_row<TB>(P, key, c8, t, o);
             }
         }
         __syncthreads();
@@ -758,9 +808,9 @@ extern "C" dllm_status dllm_embed(void *stream, const void *table, int32_t table
     P.n = n_tokens; P.n_vocab = n_vocab; P.D = D;
     P.scale = scale;
     P.status = status;
-    P.nv = vectors_of(D);
-    P.lanes_log2 = std::min(log2_up(P.nv), 6);
-    P.segs = (P.nv + 64 * kLookVecs - 1) / (64 * kLookVecs);
+    const int nv = vectors_of(D);
+    P.lanes_log2 = std::min(log2_up(nv), 6);
+    P.segs = (nv + 64 * kLookVecs - 1) / (64 * kLookVecs);
     const bool wide = P.lanes_log2 == 6;
     const int per = 64 >> P.lanes_log2;
     const int64_t units = wide ? (int64_t)n_tokens * P.segs : ((int64_t)n_tokens + per - 1) / per;
@@ -811,9 +861,8 @@ extern "C" dllm_status dllm_embed_grad(void *stream, const void *grad_out, int32
     char *ws = (char *)workspace;
     const hipStream_t st = (hipStream_t)stream;
 
-    const int nv = vectors_of(D);
     const int fill = (D * ts + 15) / 16;
-    const Table table = {(char *)grad_table, table_stride * ts, n_vocab, D, nv, fill, log2_up(fill)};
+    const Table table = {(char *)grad_table, table_stride * ts, n_vocab, D, fill, log2_up(fill)};
     const bool tb = table_dtype == DLLM_BF16, gb = grad_dtype == DLLM_BF16, old = accumulate != 0;
     SortParams S{};
     S.ids = ids; S.valid = valid;
