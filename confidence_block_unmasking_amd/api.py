@@ -314,25 +314,29 @@ def dllm_step_features(rows, L, row_req, reqs: "ReqTable", conf, mask_out, featu
 
 # ---- log probabilities and embeddings: the two sides of the forward ------------------------------
 
+_devices = 0          # GPUs this process sees (counted at the first call)
+
+
 def _call(fn, where, stream, tensors, *args):
-    """fn(stream, *args) on the device that all `tensors` share (None entries aside), whatever the
-    current device is; `stream`, when given, must be that device's.  The small calls take
-    microseconds on the device, so this path avoids building stream objects."""
-    dev = -1
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if dev < 0:
-                dev = d
-            elif d != dev:
-                raise ValueError(f"{where}: tensors on devices {dev} and {d}; all must be on one device")
+    """fn(stream, *args) on the device that all `tensors` share (None entries aside; each has been
+    checked to be a device tensor), whatever the current device is; `stream`, when given, must be that
+    device's.  The small calls take microseconds on the device, so this path avoids building stream
+    objects, and with one GPU there is nothing to compare."""
+    global _devices
+    if not _devices:
+        _devices = torch.cuda.device_count()
+    dev = tensors[0].get_device()
+    if _devices > 1:
+        for t in tensors:
+            if t is not None and t.get_device() != dev:
+                raise ValueError(f"{where}: tensors on devices {dev} and {t.get_device()}; all must be on one device")
     if stream is not None:
         if stream.device.index != dev:
             raise ValueError(f"{where}: stream of {stream.device} for tensors on device {dev}")
         handle = stream.cuda_stream
     else:
         handle = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch.cuda.current_device():
+    if _devices == 1 or dev == torch.cuda.current_device():
         rc = fn(handle, *args)
     else:
         with torch.cuda.device(dev):
@@ -350,14 +354,16 @@ def _tokens_arg(tokens, rows, L):
     stride (such as box[:, W - L:])."""
     if not tokens.is_cuda or tokens.dtype != torch.int32:
         raise ValueError(f"tokens must be an int32 device tensor, got {tokens.dtype} on {tokens.device}")
-    if tokens.dim() == 2:
-        if tokens.shape[0] < rows or tokens.shape[1] < L:
-            raise ValueError(f"tokens of shape {tuple(tokens.shape)}, needs [{rows}, {L}]")
-        if L > 1 and tokens.stride(1) != 1:
-            raise ValueError("tokens must have unit stride along a row")
-        return tokens.stride(0) if tokens.shape[0] > 1 else max(tokens.stride(0), L)
-    _need(tokens, torch.int32, "tokens", rows * L)
-    return L
+    if tokens.dim() != 2:
+        _need(tokens, torch.int32, "tokens", rows * L)
+        return L
+    have, wide = tokens.shape
+    if have < rows or wide < L:
+        raise ValueError(f"tokens of shape {tuple(tokens.shape)}, needs [{rows}, {L}]")
+    step, unit = tokens.stride()
+    if L > 1 and unit != 1:
+        raise ValueError("tokens must have unit stride along a row")
+    return step if have > 1 else max(step, L)
 
 
 def dllm_logprobs_workspace_bytes(rows: int, L: int, V: int, k: int = 0, dtype=torch.bfloat16) -> int:

@@ -309,3 +309,25 @@ def test_binding_refuses_what_the_kernels_cannot_read():
         with pytest.raises(api.DllmError):
             api.dllm_embed_grad(**{**good, **kw})
     torch.cuda.synchronize()
+
+
+def test_gradients_on_two_streams_at_once():
+    """Two tables accumulated at the same time on two streams, each with its own workspace."""
+    from confidence_block_unmasking_amd import api
+    rng = np.random.default_rng(17)
+    jobs = []
+    for n, V, D in ((20000, 3000, 264), (700, 90, 40)):
+        g, gh = _matrix(rng, n, D, "bf16")
+        ids = _ids("half-mask", n, V, rng).astype(np.int32)
+        jobs.append(dict(g=g, gh=gh, ids=ids, d=torch.from_numpy(ids).cuda(), t=torch.empty((V, D), device="cuda"),
+                         ws=api.new_embed_grad_workspace(n, V, D), st=_status(), s=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for j in jobs:
+            api.dllm_embed_grad(j["g"], j["d"], j["t"], j["ws"], j["st"], stream=j["s"])
+            api.dllm_embed_grad(j["g"], j["d"], j["t"], j["ws"], j["st"], accumulate=True, stream=j["s"])
+    torch.cuda.synchronize()
+    for j in jobs:
+        V = j["t"].shape[0]
+        ref, size, count = oembed.gradient(j["gh"], j["ids"], V)
+        check_grad(j["t"].double().cpu().numpy(), ref, 2 * size, count, "fp32", ref)

@@ -146,7 +146,7 @@ def test_optional_outputs(entropy, stats, k):
     check(g, x, mask, tokens, k)
 
 
-@pytest.mark.parametrize("rows,L,V,share", [(2000, 8, 70, 0.3), (4096, 64, 5, 0.02), (300, 64, 130, 1.0),
+@pytest.mark.parametrize("rows,L,V,share", [(2000, 8, 70, 0.3), (4096, 64, 5, 0.02), (4096, 64, 3, 1.0), (300, 64, 130, 1.0),
                                             (1024, 32, 9, 0.0)])
 def test_many_slots(rows, L, V, share):
     """More slots than one pass of the mask scan covers (8192), dense, sparse and none at all."""
