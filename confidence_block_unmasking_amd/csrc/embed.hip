@@ -18,18 +18,18 @@
 //   1. Sort: least-significant-digit radix sort of (id, position), kDigit bits a pass, as few passes as
 //      the vocabulary's bits need.  A pass counts digits per tile, then moves the items; a wave finds
 //      an item's rank among equal digits by one ballot per digit bit.  One tile: all passes in one
-//      launch.  The sort keeps few compute units busy, so each of its launches also writes zeros to a
-//      share of the table, which hides the sort entirely behind a large table; rows that do occur
-//      are written again in step 2.  (Looking up which rows occur and clearing the others beside
-//      the sums instead took 317 us for 1.25 GB of bf16 table and 64 x 544 tokens; this takes 282.)
+//      launch.  The sort keeps few compute units busy, so each of its launches also writes zeros to as
+//      much of the table as hides it; what a large table has left, a launch of its own clears faster.
+//      Rows that do occur are written again in step 2.  (Looking up which rows occur and clearing the
+//      others beside the sums instead took 317 us for 1.25 GB of bf16 table and 64 x 544 tokens.)
 //   2. Sum: one wave per piece of kPiece sorted tokens and 512 columns.  It loads kAhead tokens at a time
 //      whatever run they belong to (most runs are a token or two), adds them in order, and writes a
 //      row where a run ends.  A piece sums the runs that start in it, following the last one past its
 //      end, so runs up to kPiece tokens are never split.  A longer run (the mask token of a training
 //      box can hold half of all tokens) leaves one partial sum per piece it covers.
 //   3. Join: the partial sums of each long run, in order.
-// 64 x 544 tokens of width 4096 into 152066 bf16 rows take 288 us, of which the zeros (1.25 GB) 202 with the sort
-// behind them, the sums 75 (0.32 GB, while the last-level cache still drains zeros; 75 for 0.41 GB when
+// 64 x 544 tokens of width 4096 into 152066 bf16 rows take 285 us, of which the zeros (1.25 GB) 202 with the sort
+// behind a quarter of them, the sums 75 (0.32 GB, while the last-level cache still drains zeros; 75 for 0.41 GB when
 // accumulating), the join 8.  Two batches of 1600 tokens of width 1000 take 49 us, bound by six dependent launches.
 #include <algorithm>
 #include <type_traits>
@@ -252,9 +252,8 @@ __device__ __forceinline__ void fill_rows(const Table &T, int first, int end) {
 // ---- sort ----------------------------------------------------------------------------------------
 constexpr int kDigit = 9;
 constexpr int kBins = 1 << kDigit;
-// Threads of a sorting workgroup: kSortWide is the faster sort; kSortNarrow is the faster fill, where
-// the table is large enough for the fill to hide the sort (see launch).
-constexpr int kSortWide = 1024, kSortNarrow = 256;
+constexpr int kSortThreads = 1024;
+constexpr int kZeroThreads = 256;              // of the launch that only clears
 constexpr int kMinTile = 4096;                 // a multiple of 64 items per wave
 constexpr int kMaxTiles = 256;                 // a moving workgroup adds up the counts of the tiles before its own
 
@@ -288,7 +287,7 @@ __device__ __forceinline__ uint64_t sort_item(const SortParams &P, int i, bool r
 }
 __device__ __forceinline__ int digit_of(uint64_t item, int shift) { return (int)((item >> 32) >> shift) & (kBins - 1); }
 
-// The filling workgroups of a sort launch follow its `sorting` ones.
+// The filling workgroups of a launch follow its `sorting` ones.
 template <bool TB, int T>
 __device__ __forceinline__ bool fills(const SortParams &P, int sorting) {
     if ((int)blockIdx.x < sorting) return false;
@@ -297,8 +296,9 @@ __device__ __forceinline__ bool fills(const SortParams &P, int sorting) {
     return true;
 }
 
-template <bool FIRST, bool TB, int T>
-__global__ __launch_bounds__(T) void sort_count_kernel(SortParams P) {
+template <bool FIRST, bool TB>
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortParams P) {
+    constexpr int T = kSortThreads;
     __shared__ int s_count[kBins];
     if (fills<TB, T>(P, P.tiles)) return;
     const int tid = threadIdx.x, tile = blockIdx.x;
@@ -309,6 +309,12 @@ __global__ __launch_bounds__(T) void sort_count_kernel(SortParams P) {
     for (int i = i0 + tid; i < end; i += T) atomicAdd(&s_count[digit_of(sort_item<FIRST>(P, i, true), P.shift)], 1);
     __syncthreads();
     for (int b = tid; b < kBins; b += T) P.hist[tile * kBins + b] = s_count[b];
+}
+
+// Zeros alone: the rows that the launches of the sort leave.
+template <bool TB>
+__global__ __launch_bounds__(kZeroThreads) void embed_zero_kernel(SortParams P) {
+    fills<TB, kZeroThreads>(P, 0);
 }
 
 // Lanes of the wave that hold the same digit (only lanes with `on` count).
@@ -323,40 +329,32 @@ __device__ __forceinline__ uint64_t same_digit(int d, bool on) {
 }
 
 // The counts of a workgroup's waves, and from them where each wave's next item of each digit goes.
-template <int T>
 struct Places {
-    static constexpr int kWaves = T / 64, kThreads = T < kBins ? T : kBins, kOwn = kBins / kThreads;
+    static constexpr int kWaves = kSortThreads / 64;
     int at[kWaves][kBins];
-    int sum[kThreads / 64];
+    int sum[kBins / 64];
 
     __device__ __forceinline__ void clear() {
-        for (int b = threadIdx.x; b < kWaves * kBins; b += T) (&at[0][0])[b] = 0;
+        for (int b = threadIdx.x; b < kWaves * kBins; b += kSortThreads) (&at[0][0])[b] = 0;
     }
-    // The first kThreads threads own kOwn digits each: `total` of them in all tiles, `before` in earlier ones.
+    // Each of the first kBins threads owns a digit: `total` of it in all tiles, `before` in earlier ones.
     // An item goes behind those of smaller digits, of earlier tiles and of earlier waves.
-    __device__ __forceinline__ void place(const int (&before)[kOwn], const int (&total)[kOwn]) {
+    __device__ __forceinline__ void place(int before, int total) {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-        int all = 0, incl = 0;
-        if (tid < kThreads) {
-#pragma unroll
-            for (int o = 0; o < kOwn; ++o) all += total[o];
-            incl = wave_incl_scan(all);
+        int incl = 0;
+        if (tid < kBins) {
+            incl = wave_incl_scan(total);
             if (lane == 63) sum[wave] = incl;
         }
         __syncthreads();
-        if (tid < kThreads) {
-            int start = incl - all;
-            for (int w = 0; w < wave; ++w) start += sum[w];
+        if (tid < kBins) {
+            int to = incl - total + before;
+            for (int w = 0; w < wave; ++w) to += sum[w];
 #pragma unroll
-            for (int o = 0; o < kOwn; ++o) {
-                int to = start + before[o];
-                start += total[o];
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    const int c = at[w][tid * kOwn + o];
-                    at[w][tid * kOwn + o] = to;
-                    to += c;
-                }
+            for (int w = 0; w < kWaves; ++w) {
+                const int c = at[w][tid];
+                at[w][tid] = to;
+                to += c;
             }
         }
         __syncthreads();
@@ -379,29 +377,23 @@ struct Places {
 };
 
 // Moves a tile's items; wave w moves consecutive ones, after those of waves < w.
-template <bool FIRST, bool TB, int T>
-__global__ __launch_bounds__(T) void sort_move_kernel(SortParams P) {
-    typedef Places<T> Pl;
-    __shared__ Pl s;
-    if (fills<TB, T>(P, P.tiles)) return;
+template <bool FIRST, bool TB>
+__global__ __launch_bounds__(kSortThreads) void sort_move_kernel(SortParams P) {
+    __shared__ Places s;
+    if (fills<TB, kSortThreads>(P, P.tiles)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, mine = blockIdx.x;
     s.clear();
-    int before[Pl::kOwn], total[Pl::kOwn];
-#pragma unroll
-    for (int o = 0; o < Pl::kOwn; ++o) before[o] = total[o] = 0;
-    if (tid < Pl::kThreads) {
+    int before = 0, total = 0;
+    if (tid < kBins) {
 #pragma unroll 8
         for (int t = 0; t < P.tiles; ++t) {
-#pragma unroll
-            for (int o = 0; o < Pl::kOwn; ++o) {
-                const int c = P.hist[t * kBins + tid * Pl::kOwn + o];
-                before[o] += t < mine ? c : 0;
-                total[o] += c;
-            }
+            const int c = P.hist[t * kBins + tid];
+            before += t < mine ? c : 0;
+            total += c;
         }
     }
     __syncthreads();
-    const int share = P.tile / Pl::kWaves, w0 = mine * P.tile + wave * share;
+    const int share = P.tile / Places::kWaves, w0 = mine * P.tile + wave * share;
     for (int i = w0 + lane; i < w0 + share; i += 64)
         if (i < P.n) atomicAdd(&s.at[wave][digit_of(sort_item<FIRST>(P, i, false), P.shift)], 1);
     __syncthreads();
@@ -416,15 +408,13 @@ __global__ __launch_bounds__(T) void sort_move_kernel(SortParams P) {
 
 // One tile: every pass in one workgroup, the items in LDS between the passes.
 template <bool TB>
-__global__ __launch_bounds__(kSortWide) void sort_one_kernel(SortParams P) {
-    constexpr int T = kSortWide;
-    typedef Places<T> Pl;
-    constexpr int kHeld = kMinTile / T;        // items per thread
-    __shared__ Pl s;
+__global__ __launch_bounds__(kSortThreads) void sort_one_kernel(SortParams P) {
+    constexpr int kHeld = kMinTile / kSortThreads;   // items per thread
+    __shared__ Places s;
     __shared__ uint64_t s_item[kMinTile];
-    if (fills<TB, T>(P, 1)) return;
+    if (fills<TB, kSortThreads>(P, 1)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int share = P.tile / Pl::kWaves, w0 = wave * share;
+    const int share = P.tile / Places::kWaves, w0 = wave * share;
     if (tid == 0) *P.n_long = 0;
     uint64_t item[kHeld];
 #pragma unroll
@@ -445,16 +435,12 @@ __global__ __launch_bounds__(kSortWide) void sort_one_kernel(SortParams P) {
         for (int h = 0; h < kHeld; ++h)
             if (h * 64 < share && w0 + h * 64 + lane < P.n) atomicAdd(&s.at[wave][digit_of(item[h], shift)], 1);
         __syncthreads();
-        int before[Pl::kOwn], total[Pl::kOwn];
+        int total = 0;
+        if (tid < kBins) {
 #pragma unroll
-        for (int o = 0; o < Pl::kOwn; ++o) {
-            before[o] = total[o] = 0;
-            if (tid < Pl::kThreads) {
-#pragma unroll
-                for (int w = 0; w < Pl::kWaves; ++w) total[o] += s.at[w][tid * Pl::kOwn + o];
-            }
+            for (int w = 0; w < Places::kWaves; ++w) total += s.at[w][tid];
         }
-        s.place(before, total);
+        s.place(0, total);
         const bool last = shift + kDigit >= P.bits;
 #pragma unroll
         for (int h = 0; h < kHeld; ++h) {
@@ -721,10 +707,14 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams P) {
 
 // ---- host -----------------------------------------------------------------------------------------
 constexpr int64_t kSmallUnits = 2048;
-// Table bytes from which the narrow sort's faster fill outweighs its slower sort: 1.25 GB take 288 us with
-// it against 301 (34816 tokens), 262 and 311 MB take 132 and 84 us against 115 and 75 (two batches of 8192
-// tokens, and 16384).
-constexpr int64_t kHidingFill = 768 << 20;
+// Bytes of zeros that a launch of the sort hides: one of several, and a single one by its tokens.  Its 1024
+// threads write 6.0 TB/s, the zeros' own launch 7.0, at 2.5 us for the launch: 52 MiB left over gain nothing,
+// 97 a microsecond.  All beside the sort against this rule: 518 MB and 160 tokens 102 us and 85, 4096 tokens 104
+// and 94; 623 MB and 8192 tokens 137 and 128; 131 MB and 160 tokens 32.1 and 31.0.  Of several launches, each
+// hiding 32, 64, 96, 128 MiB takes 131, 127, 129, 134 us there, and 297, 287, 285, 288 for 1.25 GB and 34816 tokens.
+constexpr int64_t kBesideLaunch = 80 << 20, kBesideOne = 24 << 20, kBesideToken = 24 << 10;
+constexpr int64_t kApart = 80 << 20;           // zeros beyond those that are worth a launch of their own
+constexpr size_t kZeroFront = 35 << 10;        // LDS that holds four of its workgroups on a compute unit; 90 us for 85 without
 
 struct GradSpace {
     size_t a, b, hist, n_long, long_piece, part, bytes;
@@ -733,7 +723,7 @@ struct GradSpace {
 GradSpace grad_space(int64_t n, int64_t D) {
     GradSpace w{};
     // whole rounds of 64 items for each wave of the wider sort
-    w.tile = (int)std::max<int64_t>(kSortWide, std::min<int64_t>(kMinTile, (n + kSortWide - 1) / kSortWide * kSortWide));
+    w.tile = (int)std::max<int64_t>(kSortThreads, std::min<int64_t>(kMinTile, (n + kSortThreads - 1) / kSortThreads * kSortThreads));
     while ((n + w.tile - 1) / w.tile > kMaxTiles) w.tile *= 2;
     w.tiles = (int)((n + w.tile - 1) / w.tile);
     // Fewer than kSmallUnits waves at kPiece tokens leave compute units idle while each wave works through
@@ -875,44 +865,47 @@ extern "C" dllm_status dllm_embed_grad(void *stream, const void *grad_out, int32
     S.bits = 1;                                // ids 0 .. n_vocab, n_vocab itself standing for no id
     while (n_vocab >> S.bits) ++S.bits;
     const int passes = (S.bits + kDigit - 1) / kDigit;
-    // Every launch of the sort clears an even share of the table's rows.
-    const bool one = w.tiles <= 1, narrow = !one && !old && (int64_t)n_vocab * D * ts >= kHidingFill;
+    // Each launch of the sort clears an even share of the table's rows, or of those that it hides.
+    const bool one = w.tiles <= 1;
     const int launches = one ? 1 : 2 * passes;
-    const int at_once = rows_at_once(narrow ? kSortNarrow : kSortWide, table.fill_log2);
-    int launched = 0;
-    auto launch = [&](auto kernel, int threads, int sorting, size_t front) {
-        S.fill_first = old ? 0 : (int)((int64_t)n_vocab * launched / launches);
-        S.fill_end = old ? 0 : (int)((int64_t)n_vocab * ++launched / launches);
+    const int64_t zeros = old ? 0 : (int64_t)n_vocab * D * ts;
+    const int64_t beside = one ? kBesideOne + n_tokens * kBesideToken : launches * kBesideLaunch;
+    const bool apart = zeros >= beside + kApart;
+    const int sort_rows = old ? 0 : apart ? (int)(n_vocab * beside / zeros) : n_vocab;
+    auto launch = [&](auto kernel, int threads, int sorting, int rows_end, size_t front) {
+        const int at_once = rows_at_once(threads, table.fill_log2);
+        S.fill_first = S.fill_end;
+        S.fill_end = rows_end;
         const int blocks = sorting + (S.fill_end - S.fill_first + at_once - 1) / at_once;
         hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), front, st, S);
     };
-    auto sort = [&](auto width, auto bf16) {
-        constexpr int T = decltype(width)::value;
+    int launched = 0;
+    auto sort_step = [&](auto kernel, int sorting) {
+        launch(kernel, kSortThreads, sorting, (int)((int64_t)sort_rows * ++launched / launches), 0);
+    };
+    auto sort = [&](auto bf16) {
         constexpr bool B = decltype(bf16)::value;
-        // LDS on top of the kernel's own, for the fill's dense front
-        constexpr size_t count_front = T == kSortNarrow ? 32 << 10 : 0, move_front = T == kSortNarrow ? 25 << 10 : 0;
-        for (int pass = 0; pass < passes; ++pass) {
+        if (one) {
+            S.out = to;
+            sort_step(sort_one_kernel<B>, 1);
+            std::swap(from, to);
+        }
+        for (int pass = 0; pass < passes && !one; ++pass) {
             S.shift = pass * kDigit;
             S.in = from;
             S.out = to;
             if (pass == 0) {
-                launch(sort_count_kernel<true, B, T>, T, w.tiles, count_front);
-                launch(sort_move_kernel<true, B, T>, T, w.tiles, move_front);
+                sort_step(sort_count_kernel<true, B>, w.tiles);
+                sort_step(sort_move_kernel<true, B>, w.tiles);
             } else {
-                launch(sort_count_kernel<false, B, T>, T, w.tiles, count_front);
-                launch(sort_move_kernel<false, B, T>, T, w.tiles, move_front);
+                sort_step(sort_count_kernel<false, B>, w.tiles);
+                sort_step(sort_move_kernel<false, B>, w.tiles);
             }
             std::swap(from, to);
         }
+        if (apart) launch(embed_zero_kernel<B>, kZeroThreads, 0, n_vocab, kZeroFront);
     };
-    typedef std::integral_constant<int, kSortNarrow> Narrow;
-    typedef std::integral_constant<int, kSortWide> Wide;
-    if (one) {
-        S.out = to;
-        tb ? launch(sort_one_kernel<true>, kSortWide, 1, 0) : launch(sort_one_kernel<false>, kSortWide, 1, 0);
-        std::swap(from, to);
-    } else if (tb) narrow ? sort(Narrow(), std::true_type()) : sort(Wide(), std::true_type());
-    else narrow ? sort(Narrow(), std::false_type()) : sort(Wide(), std::false_type());
+    tb ? sort(std::true_type()) : sort(std::false_type());
     rc = check_hip(hipGetLastError(), "dllm_embed_grad sort launch");
     if (rc != DLLM_OK || n_tokens == 0) return rc;
 

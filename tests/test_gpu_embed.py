@@ -193,6 +193,41 @@ def test_gradient_of_a_large_table(n):
     assert not t[absent].any() and (buf[:, D:] == 776.0).all() and int(st.item()) == 0
 
 
+@pytest.mark.parametrize("n,V,D,pitch,table", [(1, 60000, 1000, 1000, "fp32"), (160, 1600000, 33, 33, "fp32"),
+                                               (700, 110000, 257, 259, "fp32"), (3000, 100001, 513, 515, "fp32"),
+                                               (4096, 90001, 2050, 2052, "bf16"), (4097, 120000, 1001, 1001, "fp32"),
+                                               (9000, 1100000, 200, 203, "bf16")])
+def test_gradient_whose_zeros_outlast_the_sort(n, V, D, pitch, table):
+    """Tables that the launches of the sort clear only in part: every row that occurs against float64 sums,
+    every other row zero, the columns past D untouched."""
+    from confidence_block_unmasking_amd import api
+    rng = np.random.default_rng(n)
+    buf = torch.full((V, pitch), 776.0, dtype=torch.bfloat16 if table == "bf16" else torch.float32, device="cuda")
+    t = buf[:, :D]
+    ids = torch.from_numpy(_ids("half-mask", n, V, rng).astype(np.int32)).cuda()
+    ids[0] = V - 1
+    g = torch.randn((n, D), device="cuda").to(torch.bfloat16)
+    st = _status()
+    api.dllm_embed_grad(g, ids, t, api.new_embed_grad_workspace(n, V, D), st, scale=0.5)
+    names, back = ids.long().unique(return_inverse=True)
+    ref = torch.zeros((names.numel(), D), dtype=torch.float64, device="cuda").index_add_(0, back, 0.5 * g.double())
+    size = torch.zeros_like(ref).index_add_(0, back, 0.5 * g.double().abs())
+    depth = torch.bincount(back).clamp(max=81 + n // 192)[:, None]
+    tol = U * (depth + 2) * size
+    assert ((t[names].double() - ref).abs() <= tol + HALF[table] * (ref.abs() + tol)).all()
+    absent = torch.ones(V, dtype=torch.bool, device="cuda")
+    absent[names] = False
+    assert not t[absent].any() and (buf[:, D:] == 776.0).all() and int(st.item()) == 0
+
+
+def test_gradient_of_a_large_table_without_tokens():
+    from confidence_block_unmasking_amd import api
+    t = torch.full((70000, 1025), 9.0, device="cuda")
+    ids = torch.zeros(0, dtype=torch.int32, device="cuda")
+    api.dllm_embed_grad(torch.ones((1, 1025), device="cuda"), ids, t, api.new_embed_grad_workspace(0, 70000, 1025), _status())
+    assert not t.any()
+
+
 def test_gradient_without_tokens():
     from confidence_block_unmasking_amd import api
     for n, valid in ((0, None), (5, torch.zeros(5, dtype=torch.uint8, device="cuda"))):
