@@ -171,7 +171,7 @@ def test_gradient(n, V, D, kind, go, table, extra, offset, accumulate):
 
 @pytest.mark.parametrize("n", [3000, 9000])
 def test_gradient_of_a_large_table(n):
-    """A table whose zeros hide the sort (from 768 MiB on): every row that occurs against float64 sums of its
+    """A table whose zeros hide the sort: every row that occurs against float64 sums of its
     tokens, every other row zero, the columns past D untouched."""
     from confidence_block_unmasking_amd import api
     rng = np.random.default_rng(n)
