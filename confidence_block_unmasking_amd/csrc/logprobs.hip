@@ -340,12 +340,11 @@ __device__ __forceinline__ Softmax join_records(const float4 *rec, int NC, float
     const float sc = __builtin_amdgcn_exp2f(d);
     w = red_sum_bc(sc * fmaf(d, s, w));
     s = red_sum_bc(sc * s);
-    // The largest term is 1 and the entropy is not negative: roundings below that are taken back.  On the
-    // bits: the library is built without NaN semantics, and a float comparison here may drop a NaN.
-    if (__float_as_uint(s) - 1u < 0x3F800000u - 1u) s = 1.0f;              // 0 < s < 1
+    // The largest term is 1 and the entropy is not negative: roundings below that are taken back (a NaN
+    // compares false and stays).
+    if (s > 0.0f && s < 1.0f) s = 1.0f;
     const float ls = logf(s), h = fmaf(-kLn2, w / s, ls);
-    const bool below = __float_as_uint(h) - 0x80000000u <= 0x7F800000u;    // sign set, no NaN
-    return {mw, ls, below ? 0.0f : h};
+    return {mw, ls, h <= 0.0f ? 0.0f : h};
 }
 // The given token's column; -1 for none, or one out of range.
 __device__ __forceinline__ int given_token(const LogprobParams &P, int slot) {
