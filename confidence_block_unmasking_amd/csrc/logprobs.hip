@@ -322,13 +322,18 @@ struct Softmax {
 
 // One wave: a slot's chunk records, each lane its own in order (the first one, record lane_id(), already
 // loaded), then the lanes by a fixed tree.  A row without a finite logit has a sum of 0: its log is
-// -inf, and -inf - -inf is the NaN reported.
+// -inf, and -inf - -inf is the NaN reported.  A NaN logit makes its chunk's sum NaN, and every sum that takes
+// it in, at weight 0 too.
 __device__ __forceinline__ Softmax join_records(const float4 *rec, int NC, float4 p) {
     float m = -INFINITY, s = 0.0f, w = 0.0f;
     for (int c = lane_id(); c < NC; c += 64) {
         if (c >= 64) p = rec[c];
         const float mm = fmaxf(m, p.x);
-        if (mm == -INFINITY) continue;
+        if (mm == -INFINITY) {                 // sums of 0, or NaN: the maximum passes over NaN
+            s += p.y;
+            w += p.z;
+            continue;
+        }
         const float da = fmaxf((m - mm) * kLog2e, kFarBelow), db = fmaxf((p.x - mm) * kLog2e, kFarBelow);
         const float ea = __builtin_amdgcn_exp2f(da), eb = __builtin_amdgcn_exp2f(db);
         w = ea * fmaf(da, s, w) + eb * fmaf(db, p.y, p.z);
