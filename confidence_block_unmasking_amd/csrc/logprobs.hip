@@ -57,9 +57,10 @@ struct LogprobParams {
     int32_t *status;
 };
 
-// Integer order of floats: larger value, larger key; -0 and +0 share one.
+// Integer order of floats: larger value, larger key; -0 and +0 share one, NaN has that of -inf.  A lane's
+// largest value passes over NaN, so one of its elements has that value's key or a larger one, whatever they are.
 __device__ __forceinline__ int order_key(float x) {
-    const int b = __float_as_int(x + 0.0f);
+    const int b = __float_as_int(x != x ? -INFINITY : x + 0.0f);
     return b ^ ((b >> 31) & 0x7FFFFFFF);
 }
 __device__ __forceinline__ float key_value(int key) { return __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF)); }

@@ -371,8 +371,8 @@ dllm_status dllm_compact(void *stream, int32_t rows, int32_t L, int32_t W, int32
  * Logits are as for dllm_step, but may hold -inf (a column that cannot be chosen: probability 0, log
  * probability -inf, no part in the entropy) and need no alignment beyond their type.  A slot whose
  * logits are all -inf, or hold NaN or +inf, reports NaN for every log probability and the entropy; if
- * it holds NaN, the order of its alternatives is not specified.  A token outside [0, V) sets
- * *status = DLLM_ERR_ARG and its logprob reads NaN.
+ * it holds NaN, the order of its alternatives is not specified (they are k different columns all the
+ * same).  A token outside [0, V) sets *status = DLLM_ERR_ARG and its logprob reads NaN.
  * tokens with logprob, entropy, stats, and top_ids with top_logprobs (k > 0) are optional, at least
  * one of them given.  0 <= k <= min(DLLM_MAX_TOP, V).  stats 8-byte aligned.
  * workspace: dllm_logprobs_workspace_bytes(rows, L, V, k, dtype) bytes, 16-byte aligned, any contents;
