@@ -748,6 +748,16 @@ GradSpace grad_space(int64_t n, int64_t D) {
     return w;
 }
 
+// What serves any box of up to n tokens.  A layout's size grows with its tokens but where their pieces get longer
+// and where a sort tile doubles (fewer counts), so those before each fall count too.
+size_t space_up_to(int64_t n, int64_t D) {
+    size_t bytes = grad_space(n, D).bytes;
+    const int64_t short_pieces = (kSmallUnits - 1) / ((D + kSumCols - 1) / kSumCols) * kPiece;
+    if (n > short_pieces) bytes = std::max(bytes, grad_space(short_pieces, D).bytes);
+    for (int64_t full = (int64_t)kMaxTiles * kMinTile; full < n; full *= 2) bytes = std::max(bytes, grad_space(full, D).bytes);
+    return bytes;
+}
+
 bool sizes_ok(int32_t n_tokens, int32_t n_vocab, int32_t D) {
     return n_tokens >= 0 && n_tokens <= DLLM_MAX_TOKENS && n_vocab >= 1 && n_vocab <= DLLM_MAX_VOCAB && D >= 1 && D <= DLLM_MAX_WIDTH;
 }
@@ -820,7 +830,7 @@ extern "C" dllm_status dllm_embed(void *stream, const void *table, int32_t table
 
 extern "C" size_t dllm_embed_grad_workspace_bytes(int32_t n_tokens, int32_t n_vocab, int32_t D) {
     if (!sizes_ok(n_tokens, n_vocab, D)) return 0;
-    return grad_space(n_tokens, D).bytes;
+    return space_up_to(n_tokens, D);
 }
 
 extern "C" dllm_status dllm_embed_grad(void *stream, const void *grad_out, int32_t grad_dtype, int64_t grad_stride,

@@ -442,8 +442,9 @@ dllm_status dllm_embed(void *stream, const void *table, int32_t table_dtype, int
  * of the tokens (the mask token of a training box holds a large one).
  * grad_out: [n_tokens, D], grad_table: [n_vocab, D], fp32 or bf16 each, with row strides; columns past
  * D are left alone.  workspace: dllm_embed_grad_workspace_bytes(n_tokens, n_vocab, D) bytes, 256-byte
- * aligned, any contents; not shared by overlapping calls.  grad_table and workspace must not overlap
- * the inputs or each other.
+ * aligned, any contents; not shared by overlapping calls.  That size never falls as n_tokens grows, and
+ * one for the largest box serves smaller ones.  grad_table and workspace must not overlap the inputs
+ * or each other.
  * Errors: as dllm_embed, plus DLLM_ERR_ARG for the workspace.  n_tokens == 0 with accumulate is a
  * no-op; without, it writes zeros. */
 size_t dllm_embed_grad_workspace_bytes(int32_t n_tokens, int32_t n_vocab, int32_t D);
