@@ -383,8 +383,8 @@ def dllm_logprobs(logits, mask, tokens, logprob, workspace, status, entropy=None
 
     logits as for dllm_step, at any alignment; tokens int32 [rows, L] (a view of the box's block
     columns will do) or None with logprob None; logprob, entropy float32 [rows, L]; stats float32
-    [rows, L, 2]; top_ids int32 and top_logprobs float32 [rows, L, k] (k: top_ids' last dimension
-    unless given).  Slots that are not selected keep what the outputs held."""
+    [rows, L, 2]; top_ids int32 and top_logprobs float32 [rows, L, k], or flat with k given (k:
+    top_ids' last dimension unless given).  Slots that are not selected keep what the outputs held."""
     rows, L, V, pos_stride, row_stride = _logits_shape(logits, rows, L, V, pos_stride, row_stride)
     _need(mask, torch.uint8, "mask", rows * L)
     _need(workspace, torch.uint8, "workspace")
@@ -401,6 +401,9 @@ def dllm_logprobs(logits, mask, tokens, logprob, workspace, status, entropy=None
                          (top_logprobs, torch.float32, "top_logprobs", rows * L * k)):
         if t is not None:
             _need(t, dt, nm, n)
+    for t, nm in ((top_ids, "top_ids"), (top_logprobs, "top_logprobs")):
+        if t is not None and k and t.dim() > 1 and t.size(-1) != k:
+            raise ValueError(f"{nm} of shape {tuple(t.shape)} for k={k}")
     _call(_lib.lib().dllm_logprobs, "dllm_logprobs", stream,
           (logits, mask, exclude, tokens, logprob, entropy, stats, top_ids, top_logprobs, workspace, status),
           _adr(logits), _DT[logits.dtype], pos_stride, row_stride, rows, L, V, _adr(mask), _adr(exclude), _adr(tokens),
