@@ -1,5 +1,5 @@
 // Element access shared by the log-probability and embedding kernels (internal; not part of the C
-// ABI): 16-byte vectors at any element alignment, and rounding to bf16.
+// ABI): 16-byte vectors at any element alignment, rounding to bf16, and the size of a launch.
 #pragma once
 
 #include "step_common.h"
@@ -27,6 +27,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const f32x2 v = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
+
+// Host: whether a launch of this many workgroups fits: a dimension of a grid holds fewer than 2^32 threads.
+inline bool launchable(int64_t blocks, int64_t threads) { return blocks * threads < (int64_t)1 << 32; }
 
 // Lane i reads lane i-1; lane 0 keeps its own.  Every lane must be active.
 __device__ __forceinline__ int up_one(int v) { return wave_dpp::mov<0x138>(v, v); }

@@ -815,7 +815,7 @@ extern "C" dllm_status dllm_embed(void *stream, const void *table, int32_t table
     const int per = 64 >> P.lanes_log2;
     const int64_t units = wide ? (int64_t)n_tokens * P.segs : ((int64_t)n_tokens + per - 1) / per;
     const int64_t blocks = (units + kLookWaves - 1) / kLookWaves;
-    if (blocks >= (int64_t)1 << 31) return fail(DLLM_ERR_SHAPE, "%s: n_tokens * D too large", who);
+    if (!launchable(blocks, 64 * kLookWaves)) return fail(DLLM_ERR_SHAPE, "%s: n_tokens * D too large", who);
     const hipStream_t st = (hipStream_t)stream;
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * kLookWaves), 0, st, P); };
     if (table_dtype == DLLM_BF16) {

@@ -924,7 +924,7 @@ extern "C" dllm_status dllm_logprobs_grad(void *stream, const void *logits, int3
     P.gl = grad_logprob; P.entropy = entropy; P.gh = grad_entropy;
     P.status = status;
     const int64_t blocks = (int64_t)rows * L * P.nseg;
-    if (blocks >= (int64_t)1 << 31) return fail(DLLM_ERR_SHAPE, "%s: rows*L*V too large", who);
+    if (!launchable(blocks, kGradThreads)) return fail(DLLM_ERR_SHAPE, "%s: rows*L*V too large", who);
     const dim3 grid((unsigned)blocks), block(kGradThreads);
     const hipStream_t st = (hipStream_t)stream;
     if (dtype == DLLM_BF16) {

@@ -403,7 +403,8 @@ dllm_status dllm_logprobs(void *stream, const void *logits, int32_t dtype, int64
  * otherwise.  A token outside [0, V) sets *status = DLLM_ERR_ARG and contributes no log-probability
  * gradient.  A slot with NaN statistics gets NaN.
  * Errors: as dllm_logprobs (there is no workspace), plus DLLM_ERR_ARG for gradient strides too small
- * or a partial overlap, and DLLM_ERR_SHAPE when rows*L*V needs 2^31 workgroups.  rows == 0 is a no-op.
+ * or a partial overlap, and DLLM_ERR_SHAPE when one launch cannot hold the box: rows*L*ceil(V / N) at
+ * 2^24 or more, with N = 4096 columns of bf16 or 2048 of fp32 (boxes of 135 GB).  rows == 0 is a no-op.
  * Work: one kernel. */
 dllm_status dllm_logprobs_grad(void *stream, const void *logits, int32_t dtype, int64_t pos_stride,
                                int64_t row_stride, int32_t rows, int32_t L, int32_t V, const uint8_t *mask,
@@ -423,7 +424,8 @@ dllm_status dllm_logprobs_grad(void *stream, const void *logits, int32_t dtype, 
  * table_stride / out_stride elements apart, aligned to their types.  out must not overlap the inputs.
  * Errors: DLLM_ERR_ARG (null required pointer, n_tokens < 0, stride < D, misaligned),
  * DLLM_ERR_SHAPE (n_tokens > DLLM_MAX_TOKENS, n_vocab outside [1, DLLM_MAX_VOCAB], D outside
- * [1, DLLM_MAX_WIDTH]), DLLM_ERR_DTYPE.  n_tokens == 0 is a no-op.  Work: one kernel. */
+ * [1, DLLM_MAX_WIDTH], or n_tokens * ceil(D / 2048) at 2^26 or more, past one launch),
+ * DLLM_ERR_DTYPE.  n_tokens == 0 is a no-op.  Work: one kernel. */
 dllm_status dllm_embed(void *stream, const void *table, int32_t table_dtype, int64_t table_stride,
                        int32_t n_vocab, int32_t D, const int32_t *ids, const uint8_t *valid,
                        int32_t n_tokens, float scale, void *out, int32_t out_dtype, int64_t out_stride,
