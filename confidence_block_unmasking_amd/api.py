@@ -349,6 +349,14 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
+def _fits(where, *sizes):
+    """Sizes past 32 bits are past every limit of the library, and would reach it modulo 2^32.  The callers
+    ask only where (a | b | ...) >> 31 is not 0: past 31 bits, or negative (which the library refuses)."""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise DllmError(_lib.DLLM_ERR_SHAPE, where, f"size {n} is past 32 bits")
+
+
 def _tokens_arg(tokens, rows, L):
     """Row stride of int32 tokens [rows, L]: a contiguous tensor, or a 2-D view with unit column
     stride (such as box[:, W - L:])."""
@@ -367,6 +375,8 @@ def _tokens_arg(tokens, rows, L):
 
 
 def dllm_logprobs_workspace_bytes(rows: int, L: int, V: int, k: int = 0, dtype=torch.bfloat16) -> int:
+    if max(rows, L, V, k) >> 31:                # past every limit
+        return 0
     return int(_lib.lib().dllm_logprobs_workspace_bytes(rows, L, V, k, _DT[dtype]))
 
 
@@ -404,6 +414,8 @@ def dllm_logprobs(logits, mask, tokens, logprob, workspace, status, entropy=None
     for t, nm in ((top_ids, "top_ids"), (top_logprobs, "top_logprobs")):
         if t is not None and k and t.dim() > 1 and t.size(-1) != k:
             raise ValueError(f"{nm} of shape {tuple(t.shape)} for k={k}")
+    if (rows | L | V | k) >> 31:
+        _fits("dllm_logprobs", rows, L, V, k)
     _call(_lib.lib().dllm_logprobs, "dllm_logprobs", stream,
           (logits, mask, exclude, tokens, logprob, entropy, stats, top_ids, top_logprobs, workspace, status),
           _adr(logits), _DT[logits.dtype], pos_stride, row_stride, rows, L, V, _adr(mask), _adr(exclude), _adr(tokens),
@@ -433,6 +445,8 @@ def dllm_logprobs_grad(logits, mask, tokens, stats, grad_logprob, grad_logits, s
                       (entropy, torch.float32, "entropy"), (grad_entropy, torch.float32, "grad_entropy")):
         if t is not None:
             _need(t, dt, nm, rows * L)
+    if (rows | L | V) >> 31:
+        _fits("dllm_logprobs_grad", rows, L, V)
     _call(_lib.lib().dllm_logprobs_grad, "dllm_logprobs_grad", stream,
           (logits, mask, exclude, tokens, stats, grad_logprob, entropy, grad_entropy, grad_logits, status),
           _adr(logits), _DT[logits.dtype], pos_stride, row_stride, rows, L, V, _adr(mask), _adr(exclude), _adr(tokens),
@@ -477,12 +491,16 @@ def dllm_embed(table, ids, out, status, valid=None, scale=1.0, stream=None):
     n_out, D_out, os_ = _matrix(out, "out")
     if D_out != D or n_out < n:
         raise ValueError(f"out holds {n_out} rows of {D_out}, needs {n} of {D}")
+    if (n | n_vocab | D) >> 31:
+        _fits("dllm_embed", n, n_vocab, D)
     _call(_lib.lib().dllm_embed, "dllm_embed", stream, (table, ids, valid, out, status),
           _adr(table), _DT[table.dtype], ts, n_vocab, D, _adr(ids), _adr(valid), n, float(scale), _adr(out),
           _DT[out.dtype], os_, _adr(status))
 
 
 def dllm_embed_grad_workspace_bytes(n_tokens: int, n_vocab: int, D: int) -> int:
+    if max(n_tokens, n_vocab, D) >> 31:         # past every limit
+        return 0
     return int(_lib.lib().dllm_embed_grad_workspace_bytes(n_tokens, n_vocab, D))
 
 
@@ -501,6 +519,8 @@ def dllm_embed_grad(grad_out, ids, grad_table, workspace, status, valid=None, sc
     if D_grad != D or n_grad < n:
         raise ValueError(f"grad_out holds {n_grad} rows of {D_grad}, needs {n} of {D}")
     _need(workspace, torch.uint8, "workspace")
+    if (n | n_vocab | D) >> 31:
+        _fits("dllm_embed_grad", n, n_vocab, D)
     _call(_lib.lib().dllm_embed_grad, "dllm_embed_grad", stream,
           (grad_out, ids, valid, grad_table, workspace, status),
           _adr(grad_out), _DT[grad_out.dtype], gs, _adr(ids), _adr(valid), n, float(scale), n_vocab, D,
