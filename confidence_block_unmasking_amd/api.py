@@ -73,6 +73,8 @@ def _logits_shape(logits, rows, L, V, pos_stride, row_stride):
         raise ValueError("logits must be a device tensor")
     if rows is None:
         rows, L, V = logits.shape
+    if pos_stride is None and row_stride is None and logits.dim() != 3 and not logits.is_contiguous():
+        raise ValueError(f"logits of shape {tuple(logits.shape)} with strides {logits.stride()} need pos_stride and row_stride")
     if pos_stride is None:
         pos_stride = logits.stride(1) if logits.dim() == 3 else V
     if row_stride is None:
