@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import DllmError, Meta, Queue, Reqs  # noqa: F401  (re-exported)
+from ._lib import MAX_TOP, DllmError, Meta, Queue, Reqs  # noqa: F401  (re-exported)
 
 _DT = {torch.bfloat16: _lib.DLLM_BF16, torch.float32: _lib.DLLM_FP32}
 

@@ -190,7 +190,7 @@ class Session:
     # ---- the two sides of the forward -------------------------------------------------------------
     def embed(self, table, scale=1.0, out=None):
         """The current box's embeddings [rows, W, D] from `table` [n_vocab, D] (n_vocab > mask_id), zeros
-        in the padding, for a forward to start from.  out: a buffer for them (any float type), or
+        in the padding, for a forward to start from.  out: a buffer for them (fp32 or bf16), or
         a new tensor of the table's type."""
         D = table.shape[1]
         if out is None:
@@ -201,7 +201,9 @@ class Session:
 
     def record_logprobs(self, k=0):
         """Keep, from now on, the log probability, entropy and k top alternatives of every token a step
-        unmasks (read back with logprobs())."""
+        unmasks (read back with logprobs()); 0 <= k <= min(V, 32)."""
+        if not 0 <= k <= min(self.V, api.MAX_TOP):
+            raise ValueError(f"k={k} outside [0, {min(self.V, api.MAX_TOP)}]")
         n, dev = self.reqs.n_req * self.K_max, self.device
         nan = float("nan")
         rec = dict(logprob=torch.full((n, self.L), nan, dtype=torch.float32, device=dev),
