@@ -394,8 +394,10 @@ dllm_status dllm_logprobs(void *stream, const void *logits, int32_t dtype, int64
  * For every selected slot, with p_v = exp(x_v - stats[0] - stats[1]), gl = grad_logprob[r, j], gh =
  * grad_entropy[r, j] and H = entropy[r, j]:
  *   grad_logits[r, j, v] = gl ((v == token) - p_v) - gh p_v (log p_v + H),
- * computed in float32 and rounded once to the logits' type; columns with x = -inf get 0.  Every slot
- * that is not selected is written as zeros; columns past V of a strided row are left alone.
+ * computed in float32 and rounded once to the logits' type.  A column with x = -inf has p = 0 and gets 0,
+ * or gl where it is the given token's own, as the formula says (a caller that wants none there clears
+ * grad_logprob at slots whose logprob is -inf).  Every slot that is not selected is
+ * written as zeros; columns past V of a strided row are left alone.
  * stats and entropy are the forward's outputs for the same logits (entropy may be NULL without
  * grad_entropy).  tokens with grad_logprob, and grad_entropy, are optional, at least one given.
  * grad_logits has the logits' type and strides of its own (in elements); it may be the logits
