@@ -15,8 +15,12 @@
 //     y = (x - m) log2 e and e = 2^y: the entropy costs a max and an FMA per element beside the
 //     unpack, max3, FMA, v_exp and add of the sum.  All terms of T have one sign, so the entropy
 //     has no cancellation.
-//   - y is one FMA, x*log2e - m*log2e.  The product m*log2e is rounded once per chunk; its residual r
-//     (exact, by an FMA) is taken out of the sums by a factor 2^-r, so large offsets of the logits
+//   - S is held as r = S - 1, what it has beside the largest term, through chunks, lanes and log(1 + r): a token of
+//     probability near 1 has log probability -r, of which 1 + r would keep the bits above 2^-24 only.  A
+//     chunk's r is S - 1 where S >= 1.25; below, the lane that has the maximum hands its values to the wave, which
+//     adds all but that one (0.2 to 0.4 us of 24 for 192 confident slots; 16384 slots 812 us for 812).
+//   - y is one FMA, x*log2e - m*log2e.  The product m*log2e is rounded once per chunk; its residual
+//     (exact, by an FMA) is taken out of the sums by a factor 2^-residual, so large offsets of the logits
 //     cost no accuracy.  Chunks whose maximum lies beyond kNearMax subtract first instead.
 //   - Alternatives: while a chunk is in registers each lane's largest element is known anyway; it is
 //     kept (2 or 4 bytes per 128-byte lane share).  The k-th largest of those maxima cannot exceed the
@@ -39,6 +43,7 @@ using namespace dllm;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFarBelow = -300.0f;           // base-2 exponent whose power is 0 in fp32 (2^-149 is the least)
 constexpr float kNearMax = 65536.0f;           // |m| up to which rounding m * log2e moves y by less than 2^-8
+constexpr float kPeaked = 1.25f;               // sum of powers of a chunk below which its largest element is set apart
 constexpr int kNoKey = (int)0x80000000;        // below the key of every number
 
 struct LogprobParams {
@@ -195,10 +200,11 @@ __device__ __forceinline__ const char *slot_row(const LogprobParams &P, int slot
     return P.logits + (int64_t)r * P.row_stride_b + (int64_t)j * P.pos_stride_b;
 }
 
-// A chunk's record {max, sum, weighted sum} from its values, which it may overwrite; lm: this lane's
-// largest value.
+// A chunk's record {max, sum - 1, weighted sum} from its values, which it may overwrite; lm: this lane's
+// largest value; spread: 64 values of LDS of this wave's own.  The sum's largest term is 1: without it the sum of
+// the others keeps its own bits, which is all there is to a token of probability near 1.
 template <int E, bool ENT>
-__device__ __forceinline__ float4 chunk_record(float (&x)[kVPL][E], float &lm) {
+__device__ __forceinline__ float4 chunk_record(float (&x)[kVPL][E], float &lm, float *spread) {
     lm = x[0][0];
 #pragma unroll
     for (int kk = 0; kk < kVPL; ++kk) {
@@ -231,9 +237,34 @@ __device__ __forceinline__ float4 chunk_record(float (&x)[kVPL][E], float &lm) {
     }
     const float r = fmaf(near, kLog2e, nml);   // what rounding nml added to every y
     const float back = __builtin_amdgcn_exp2f(-r);
-    const float s1 = red_sum_bc((s4[0] + s4[1]) + (s4[2] + s4[3]));
-    const float w = ENT ? fmaf(-r, s1, red_sum_bc((w4[0] + w4[1]) + (w4[2] + w4[3]))) * back : 0.0f;
-    return make_float4(m, s1 * back, w, 0.0f);
+    float s = (s4[0] + s4[1]) + (s4[2] + s4[3]), w = (w4[0] + w4[1]) + (w4[2] + w4[3]);
+    const float sum = red_sum_bc(s), s1 = sum * back;
+    if (s1 > 0.0f && s1 < kPeaked) {           // one element outweighs all others: add those alone
+        const int owner = (int)__builtin_ctzll(__ballot(lm == m));
+        const int lane = lane_id();
+        if (lane == owner) {
+#pragma unroll
+            for (int kk = 0; kk < kVPL; ++kk) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) spread[kk * E + e] = x[kk][e];
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const float v = lane < kVPL * E ? spread[lane] : -INFINITY;    // lane i: the owner's i-th element
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();       // read before the wave's next such chunk writes
+        const int largest = (int)__builtin_ctzll(__ballot(v == near));
+        const float y = fmaf(v, kLog2e, nml);
+        const float p = lane == largest ? 0.0f : __builtin_amdgcn_exp2f(y);
+        s = (lane == owner ? 0.0f : s) + p;
+        const float others = red_sum_bc(s);
+        if (ENT) w = fmaf(-r, others, red_sum_bc((lane == owner ? 0.0f : w) + p * fmaxf(y, kFarBelow))) * back;
+        return make_float4(m, others * back, w, 0.0f);
+    }
+    // s1 - 1 is exact below 2 and off by no more than s1 itself beyond
+    if (ENT) w = fmaf(-r, sum, red_sum_bc(w)) * back;
+    return make_float4(m, s1 - 1.0f, w, 0.0f);
 }
 
 // Kernel 1: one record per chunk of every selected slot, and its lanes' maxima.  Bound by HBM: 1005 slots of
@@ -244,6 +275,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
     extern __shared__ int s_id[];              // [win] selected slots of this workgroup's window
     __shared__ int s_tmp[2][kWaves];
     __shared__ int s_next;
+    __shared__ float s_spread[kWaves][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = uni(tid >> 6);
     const int NC = P.NC;
@@ -292,7 +324,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
             issue_chunk<BF16>(raw, row, cn * kCH, whole(cn), V);
         }
         float lm;
-        const float4 rec = chunk_record<E, ENT>(x, lm);
+        const float4 rec = chunk_record<E, ENT>(x, lm, s_spread[wave]);
         if (TOP) {
             char *to = P.lane_max + (int64_t)at * (64 * (16 / E));
             if (BF16) ((uint16_t *)to)[lane] = (uint16_t)(__float_as_uint(lm) >> 16);
@@ -326,30 +358,29 @@ struct Softmax {
 // -inf, and -inf - -inf is the NaN reported.  A NaN logit makes its chunk's sum NaN, and every sum that takes
 // it in, at weight 0 too.
 __device__ __forceinline__ Softmax join_records(const float4 *rec, int NC, float4 p) {
-    float m = -INFINITY, s = 0.0f, w = 0.0f;
+    float m = -INFINITY, t = -1.0f, w = 0.0f;  // the sum of powers is 1 + t
     for (int c = lane_id(); c < NC; c += 64) {
         if (c >= 64) p = rec[c];
         const float mm = fmaxf(m, p.x);
         if (mm == -INFINITY) {                 // sums of 0, or NaN: the maximum passes over NaN
-            s += p.y;
+            t += 1.0f + p.y;
             w += p.z;
             continue;
         }
         const float da = fmaxf((m - mm) * kLog2e, kFarBelow), db = fmaxf((p.x - mm) * kLog2e, kFarBelow);
         const float ea = __builtin_amdgcn_exp2f(da), eb = __builtin_amdgcn_exp2f(db);
-        w = ea * fmaf(da, s, w) + eb * fmaf(db, p.y, p.z);
-        s = ea * s + eb * p.y;
+        w = ea * fmaf(da, 1.0f + t, w) + eb * fmaf(db, 1.0f + p.y, p.z);
+        t = p.x > m ? fmaf(ea, 1.0f + t, p.y) : fmaf(eb, 1.0f + p.y, t);
         m = mm;
     }
     const float mw = red_max_bc(m);
     const float d = mw == -INFINITY ? 0.0f : fmaxf((m - mw) * kLog2e, kFarBelow);
     const float sc = __builtin_amdgcn_exp2f(d);
-    w = red_sum_bc(sc * fmaf(d, s, w));
-    s = red_sum_bc(sc * s);
-    // The largest term is 1 and the entropy is not negative: roundings below that are taken back (a NaN
-    // compares false and stays).
-    if (s > 0.0f && s < 1.0f) s = 1.0f;
-    const float ls = logf(s), h = fmaf(-kLn2, w / s, ls);
+    w = red_sum_bc(sc * fmaf(d, 1.0f + t, w));
+    const int owner = (int)__builtin_ctzll(__ballot(m == mw));
+    t = red_sum_bc(lane_id() == owner ? t : sc * (1.0f + t));
+    // A NaN compares false and stays.
+    const float ls = log1pf(t), h = fmaf(-kLn2, w / (1.0f + t), ls);
     return {mw, ls, h <= 0.0f ? 0.0f : h};
 }
 // The given token's column; -1 for none, or one out of range.
@@ -600,6 +631,7 @@ constexpr int kShortRow = 16;                  // chunks of a row at most
 template <bool BF16, bool ENT, bool TOP>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void logprob_rows_kernel(LogprobParams P) {
     __shared__ float4 s_rec[kShortRow];
+    __shared__ float s_spread[kWaves][64];
     __shared__ int s_key[TOP ? kShortRow : 1][64];
     __shared__ TopShared<kWaves> sh;
     const int lane = lane_id(), wave = uni(threadIdx.x >> 6), slot = blockIdx.x;
@@ -621,7 +653,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
         widen<BF16>(raw, x, row, whole(c), V);
         if (c + kWaves < NC) issue_chunk<BF16>(raw, row, (c + kWaves) * kCH, whole(c + kWaves), V);
         float lm;
-        const float4 rec = chunk_record<E, ENT>(x, lm);
+        const float4 rec = chunk_record<E, ENT>(x, lm, s_spread[wave]);
         if (lane == 0) s_rec[c] = rec;
         if (TOP) s_key[c][lane] = order_key(lm);
     }
