@@ -41,6 +41,7 @@ namespace {
 using namespace dllm;
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2eShort = 1.3349758e-8f;   // (log2 e - kLog2e) / kLog2e
 constexpr float kFarBelow = -300.0f;           // base-2 exponent whose power is 0 in fp32 (2^-149 is the least)
 constexpr float kNearMax = 65536.0f;           // |m| up to which rounding m * log2e moves y by less than 2^-8
 constexpr float kPeaked = 1.25f;               // sum of powers of a chunk below which its largest element is set apart
@@ -379,9 +380,12 @@ __device__ __forceinline__ Softmax join_records(const float4 *rec, int NC, float
     w = red_sum_bc(sc * fmaf(d, 1.0f + t, w));
     const int owner = (int)__builtin_ctzll(__ballot(m == mw));
     t = red_sum_bc(lane_id() == owner ? t : sc * (1.0f + t));
-    // A NaN compares false and stays.
-    const float ls = log1pf(t), h = fmaf(-kLn2, w / (1.0f + t), ls);
-    return {mw, ls, h <= 0.0f ? 0.0f : h};
+    // Powers of 2^(log2e as a float) are powers of a base a little below e; with kLog2eShort of itself more in the
+    // exponents, log S moves by that much of the mean of x - m.  (The entropy moves by as much of the variance
+    // only.  A call without entropy has no such mean, its w is 0, and keeps log S as it is: high by 0.22 of 2^-24 of
+    // the mean |x - m|.)  A NaN compares false and stays.
+    const float ls = log1pf(t), u = kLn2 * (w / (1.0f + t)), h = ls - u;
+    return {mw, fmaf(kLog2eShort, u, ls), h <= 0.0f ? 0.0f : h};
 }
 // The given token's column; -1 for none, or one out of range.
 __device__ __forceinline__ int given_token(const LogprobParams &P, int slot) {

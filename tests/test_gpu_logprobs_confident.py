@@ -76,3 +76,22 @@ def test_confident_slots(rows, V, dtype, offset, entropy, k):
         if entropy:
             tolH = U * (2.3 * (E2 / E1 if E1 > 0 else 0.0) + 160) * H + TINY * V * 128
             assert abs(got["entropy"][i] - H) <= tolH, (i, H, got["entropy"][i], (got["entropy"][i] - H) / (U * H + 1e-45))
+
+
+@pytest.mark.parametrize("d", [20, 30])
+def test_log_sums_err_to_both_sides(d):
+    """Over many slots the relative error of r averages out: roundings have no sign.  Powers of 2 with
+    log2 e as one float, which is 1.33e-8 of itself (0.224 u) too small, would make every term too large
+    by 0.224 u |x - m|: 0.224 d u on average.  At most half of that is left."""
+    n, V = 200, 126464
+    rng = np.random.default_rng(d)
+    x = (rng.standard_normal((n, V), np.float32) - np.float32(d))
+    x[np.arange(n), rng.integers(0, V, n)] = 0.0
+    x += (8 * rng.random((n, 1)) - 4).astype(np.float32)
+    t = torch.from_numpy(x)
+    g, st = run(t.view(-1).cuda(), 1, n, V, V, 0, np.ones((1, n), bool), np.zeros((1, n)), 0)
+    assert st == 0
+    ls = np.array([_reference(v.astype(np.float64))[1] for v in x])
+    rel = (g["stats"][0, :, 1] - ls) / (U * ls)
+    print(f"mean relative error {rel.mean():.2f} u, std {rel.std():.2f} u", flush=True)
+    assert abs(rel.mean()) <= 0.112 * d
