@@ -222,9 +222,10 @@ struct Table {
 
 // Rows a workgroup of `threads` clears: its threads lie along one row, or several narrow ones, one store
 // each for rows up to 16 bytes a thread.  What counts is that the stores in flight form a dense front in
-// the table: over 1.25 GB, one 16-byte store per thread in workgroups of 256 writes 6.6 TB/s, and 7.0 with
-// 33 to 40 KB of LDS each, which holds four of them on a compute unit; 1024 threads 6.0, two stores per
-// thread 5.9.  Non-temporal, so the zeros leave the last-level cache to the sums.
+// the table.  One 16-byte store per thread in workgroups of 256 with 35 KB of LDS each, which holds four of them on
+// a compute unit, clears 1.22 GB in 191 us = 6.4 TB/s (best 6.85), without that LDS in 202 = 6.0, and 0.91 GB behind
+// the sort in 142 us = 6.4 (6.0 without); 1024 threads write 6.0, two stores per thread 5.9.  Non-temporal, so the
+// zeros leave the last-level cache to the sums.
 constexpr int rows_at_once(int threads, int fill_log2) { return (1 << fill_log2) < threads ? threads >> fill_log2 : 1; }
 
 template <bool TB, int THREADS>
@@ -708,13 +709,13 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumParams P) {
 // ---- host -----------------------------------------------------------------------------------------
 constexpr int64_t kSmallUnits = 2048;
 // Bytes of zeros that a launch of the sort hides: one of several, and a single one by its tokens.  Its 1024
-// threads write 6.0 TB/s, the zeros' own launch 7.0, at 2.5 us for the launch: 52 MiB left over gain nothing,
-// 97 a microsecond.  All beside the sort against this rule: 518 MB and 160 tokens 102 us and 85, 4096 tokens 104
+// threads write 6.0 TB/s, the zeros' own launch 6.4 (and what the last-level cache takes in of a smaller table), at
+// 2.5 us for the launch: 52 MiB left over gain nothing, 97 a microsecond.  All beside the sort against this rule: 518 MB and 160 tokens 102 us and 85, 4096 tokens 104
 // and 94; 623 MB and 8192 tokens 137 and 128; 131 MB and 160 tokens 32.1 and 31.0.  Of several launches, each
 // hiding 32, 64, 96, 128 MiB takes 131, 127, 129, 134 us there, and 297, 287, 285, 288 for 1.25 GB and 34816 tokens.
 constexpr int64_t kBesideLaunch = 80 << 20, kBesideOne = 24 << 20, kBesideToken = 24 << 10;
 constexpr int64_t kApart = 80 << 20;           // zeros beyond those that are worth a launch of their own
-constexpr size_t kZeroFront = 35 << 10;        // LDS that holds four of its workgroups on a compute unit; 90 us for 85 without
+constexpr size_t kZeroFront = 35 << 10;        // LDS that holds four of its workgroups on a compute unit; 518 MB: 85 us, 90 without
 
 struct GradSpace {
     size_t a, b, hist, n_long, long_piece, part, bytes;
