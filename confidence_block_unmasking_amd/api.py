@@ -483,16 +483,25 @@ def _ids_arg(ids, valid, status):
     return ids.numel()
 
 
+def _same_box(t, name, n_rows, ids, n):
+    """Refuse a box [..., W', D] whose rows of W' are not the ids' rows: its first n of n_rows rows of D are used as
+    one run.  (A matrix [n_rows, D], or as many rows as ids, leaves no doubt; flat ids may be any whole rows.)"""
+    if t.dim() > 2 and n_rows != n:
+        if (t.shape[1:-1] != ids.shape[1:]) if ids.dim() > 1 else (n % max(t.shape[-2], 1) != 0):
+            raise ValueError(f"{name} of shape {tuple(t.shape)} for ids of shape {tuple(ids.shape)}")
+
+
 def dllm_embed(table, ids, out, status, valid=None, scale=1.0, stream=None):
     """out[n] = scale * table[ids[n]], zeros where valid[n] == 0 (see include/dllm.h).  table
     [n_vocab, D]; ids int32 and valid uint8 of any shape (a box's box_ids and box_valid); out
-    [ids.numel(), D] or ids' shape with D appended; fp32 or bf16 each.  Rows of out past the last
-    token keep what they held."""
+    [ids.numel(), D] or ids' shape with D appended, or more such rows; fp32 or bf16 each.  Rows of out
+    past the last token keep what they held."""
     n = _ids_arg(ids, valid, status)
     n_vocab, D, ts = _matrix(table, "table")
     n_out, D_out, os_ = _matrix(out, "out")
     if D_out != D or n_out < n:
         raise ValueError(f"out holds {n_out} rows of {D_out}, needs {n} of {D}")
+    _same_box(out, "out", n_out, ids, n)
     if (n | n_vocab | D) >> 31:
         _fits("dllm_embed", n, n_vocab, D)
     _call(_lib.lib().dllm_embed, "dllm_embed", stream, (table, ids, valid, out, status),
@@ -520,6 +529,7 @@ def dllm_embed_grad(grad_out, ids, grad_table, workspace, status, valid=None, sc
     n_grad, D_grad, gs = _matrix(grad_out, "grad_out")
     if D_grad != D or n_grad < n:
         raise ValueError(f"grad_out holds {n_grad} rows of {D_grad}, needs {n} of {D}")
+    _same_box(grad_out, "grad_out", n_grad, ids, n)
     _need(workspace, torch.uint8, "workspace")
     if (n | n_vocab | D) >> 31:
         _fits("dllm_embed_grad", n, n_vocab, D)

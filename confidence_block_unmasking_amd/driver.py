@@ -190,13 +190,12 @@ class Session:
     # ---- the two sides of the forward -------------------------------------------------------------
     def embed(self, table, scale=1.0, out=None):
         """The current box's embeddings [rows, W, D] from `table` [n_vocab, D] (n_vocab > mask_id), zeros
-        in the padding, for a forward to start from.  out: a buffer for them (fp32 or bf16), or
-        a new tensor of the table's type."""
+        in the padding, for a forward to start from.  out: a buffer for them (fp32 or bf16;
+        [..., W, D], or [n, D] with n at least rows * W), or a new tensor of the table's type."""
         D = table.shape[1]
         if out is None:
             out = torch.empty((self.rows, self.W, D), dtype=table.dtype, device=self.device)
-        n = self.rows * self.W
-        api.dllm_embed(table, self.box_ids[:n], out, self.status, valid=self.box_valid[:n], scale=scale)
+        api.dllm_embed(table, self.box(), out, self.status, valid=self.box_valid[:self.rows * self.W], scale=scale)
         return out
 
     def record_logprobs(self, k=0):

@@ -1,0 +1,68 @@
+"""Boxes of embeddings and of their gradients wider than the ids' box: rows would be written and read W apart
+where the buffer has them further apart, and are refused."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _inputs(rows=3, W=5, V=11, D=8):
+    g = torch.Generator().manual_seed(0)
+    return dict(ids=torch.randint(0, V, (rows, W), generator=g, dtype=torch.int32).cuda(), table=torch.randn((V, D), generator=g).cuda(),
+                status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("shape", [(3, 7, 8), (3, 6, 8), (2, 3, 8, 8), (4, 8, 8)])
+def test_wider_boxes_are_refused(shape):
+    from confidence_block_unmasking_amd import api
+    a = _inputs()
+    for ids in (a["ids"], a["ids"].view(-1)):
+        out = torch.full(shape, 7.0, device="cuda")
+        with pytest.raises(ValueError):
+            api.dllm_embed(a["table"], ids, out, a["status"])
+        grad = torch.full_like(a["table"], 7.0)
+        with pytest.raises(ValueError):
+            api.dllm_embed_grad(out, ids, grad, api.new_embed_grad_workspace(15, 11, 8), a["status"])
+        torch.cuda.synchronize()
+        assert (out == 7.0).all() and (grad == 7.0).all()
+
+
+@pytest.mark.parametrize("ids_shape,shape", [((3, 5), (3, 5, 8)), ((3, 5), (15, 8)), ((3, 5), (20, 8)), ((15,), (3, 5, 8)),
+                                             ((3, 5), (4, 5, 8)), ((3, 5), (5, 3, 8)), ((15,), (15, 8))])
+def test_layouts_that_hold_the_box(ids_shape, shape):
+    from confidence_block_unmasking_amd import api
+    a = _inputs()
+    ids = a["ids"].view(ids_shape)
+    out = torch.full(shape, 7.0, device="cuda")
+    api.dllm_embed(a["table"], ids, out, a["status"])
+    flat = out.view(-1, 8)
+    assert torch.equal(flat[:15], a["table"][a["ids"].view(-1).long()]) and (flat[15:] == 7.0).all()
+    grad = torch.full_like(a["table"], 7.0)
+    api.dllm_embed_grad(out, ids, grad, api.new_embed_grad_workspace(15, 11, 8), a["status"])
+    ref = torch.zeros_like(grad).index_add_(0, a["ids"].view(-1).long(), flat[:15])
+    assert torch.allclose(grad, ref, rtol=2.0 ** -20, atol=2.0 ** -20)
+    assert int(a["status"].item()) == 0
+
+
+def test_session_embeds_into_a_buffer_of_its_width_only():
+    from confidence_block_unmasking_amd.driver import Session
+    from workload import configs
+    w = configs.small(L=8, V=50, n_act=6, n_q=0, K=2, seed=3, dtype="fp32")
+    s = Session.from_workload(w)
+    s.compact(with_box=False)
+    s.pack()
+    table = torch.randn((w.V + 1, 24), device="cuda")
+    ref = s.embed(table)
+    buf = torch.full((s.rows_cap + 1, s.W, 24), 7.0, device="cuda")
+    s.embed(table, out=buf)
+    assert torch.equal(buf[:s.rows], ref) and (buf[s.rows:] == 7.0).all()
+    with pytest.raises(ValueError):
+        s.embed(table, out=torch.empty((s.rows, s.W + 3, 24), device="cuda"))
+    s.check_status("dllm_embed")
