@@ -38,7 +38,9 @@ def _launch(fn, args, where, events, stream):
     _lib.check(rc, where)
 
 
-def _need(t, dtype, name, numel=None):
+def _need(t, dtype, name, numel=None, inner=()):
+    """Refuse t unless it is a contiguous device tensor of this type with at least numel elements, and, where it has
+    more than those, rows of `inner` (as far as it has dimensions behind the first; flat tensors have none)."""
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -47,8 +49,12 @@ def _need(t, dtype, name, numel=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() < numel:
-        raise ValueError(f"{name} holds {t.numel()} elements, needs {numel}")
+    if numel is not None and t.numel() != numel:
+        if t.numel() < numel:
+            raise ValueError(f"{name} holds {t.numel()} elements, needs {numel}")
+        n = min(t.dim() - 1, len(inner))
+        if n > 0 and tuple(t.shape[-n:]) != tuple(inner[-n:]):
+            raise ValueError(f"{name} of shape {tuple(t.shape)} for rows of {tuple(inner)}")
 
 
 def dllm_step_workspace_bytes(rows: int, L: int, V: int, dtype=torch.bfloat16) -> int:
@@ -398,24 +404,22 @@ def dllm_logprobs(logits, mask, tokens, logprob, workspace, status, entropy=None
     [rows, L, 2]; top_ids int32 and top_logprobs float32 [rows, L, k], or flat with k given (k:
     top_ids' last dimension unless given).  Slots that are not selected keep what the outputs held."""
     rows, L, V, pos_stride, row_stride = _logits_shape(logits, rows, L, V, pos_stride, row_stride)
-    _need(mask, torch.uint8, "mask", rows * L)
+    _need(mask, torch.uint8, "mask", rows * L, (L,))
     _need(workspace, torch.uint8, "workspace")
     _need(status, torch.int32, "status", 1)
     if exclude is not None:
-        _need(exclude, torch.uint8, "exclude", rows * L)
+        _need(exclude, torch.uint8, "exclude", rows * L, (L,))
     token_stride = L
     if tokens is not None:
         token_stride = _tokens_arg(tokens, rows, L)
     if k is None:
         k = top_ids.shape[-1] if top_ids is not None else 0
-    for t, dt, nm, n in ((logprob, torch.float32, "logprob", rows * L), (entropy, torch.float32, "entropy", rows * L),
-                         (stats, torch.float32, "stats", rows * L * 2), (top_ids, torch.int32, "top_ids", rows * L * k),
-                         (top_logprobs, torch.float32, "top_logprobs", rows * L * k)):
+    n = rows * L
+    for t, dt, nm, each, inner in ((logprob, torch.float32, "logprob", 1, (L,)), (entropy, torch.float32, "entropy", 1, (L,)),
+                                   (stats, torch.float32, "stats", 2, (L, 2)), (top_ids, torch.int32, "top_ids", k, (L, k)),
+                                   (top_logprobs, torch.float32, "top_logprobs", k, (L, k))):
         if t is not None:
-            _need(t, dt, nm, n)
-    for t, nm in ((top_ids, "top_ids"), (top_logprobs, "top_logprobs")):
-        if t is not None and k and t.dim() > 1 and t.size(-1) != k:
-            raise ValueError(f"{nm} of shape {tuple(t.shape)} for k={k}")
+            _need(t, dt, nm, n * each, inner if each else ())
     if (rows | L | V | k) >> 31:
         _fits("dllm_logprobs", rows, L, V, k)
     _call(_lib.lib().dllm_logprobs, "dllm_logprobs", stream,
@@ -437,8 +441,8 @@ def dllm_logprobs_grad(logits, mask, tokens, stats, grad_logprob, grad_logits, s
     if grad_logits.dim() == 3 and tuple(grad_logits.shape) != (rows, L, V):
         raise ValueError(f"grad_logits of shape {tuple(grad_logits.shape)}, needs [{rows}, {L}, {V}]")
     _, _, _, grad_pos_stride, grad_row_stride = _logits_shape(grad_logits, rows, L, V, grad_pos_stride, grad_row_stride)
-    _need(mask, torch.uint8, "mask", rows * L)
-    _need(stats, torch.float32, "stats", rows * L * 2)
+    _need(mask, torch.uint8, "mask", rows * L, (L,))
+    _need(stats, torch.float32, "stats", rows * L * 2, (L, 2))
     _need(status, torch.int32, "status", 1)
     token_stride = L
     if tokens is not None:
@@ -446,7 +450,7 @@ def dllm_logprobs_grad(logits, mask, tokens, stats, grad_logprob, grad_logits, s
     for t, dt, nm in ((exclude, torch.uint8, "exclude"), (grad_logprob, torch.float32, "grad_logprob"),
                       (entropy, torch.float32, "entropy"), (grad_entropy, torch.float32, "grad_entropy")):
         if t is not None:
-            _need(t, dt, nm, rows * L)
+            _need(t, dt, nm, rows * L, (L,))
     if (rows | L | V) >> 31:
         _fits("dllm_logprobs_grad", rows, L, V)
     _call(_lib.lib().dllm_logprobs_grad, "dllm_logprobs_grad", stream,
