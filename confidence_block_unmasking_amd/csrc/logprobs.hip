@@ -675,8 +675,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
 // d/dx_v of gl * logprob + gh * entropy = gl (v == token) - p_v (gl + gh (log p_v + entropy)), with
 // p_v = exp(x_v - m - log S) from the forward's statistics: one read of the selected slots' logits
 // and one write of every slot's gradient (zeros where a slot is not selected).  Elementwise, bound
-// by HBM; per element an unpack, a subtraction, an FMA, v_exp, a multiplication (with entropy also a
-// max and an FMA) and half a pack.  A thread reads its vectors before it writes them, so the gradient
+// by HBM; per element an unpack, a subtraction, an FMA, a max, v_exp, an FMA and two multiplications (with entropy
+// also an FMA) and half a pack.  A thread reads its vectors before it writes them, so the gradient
 // may replace the logits in place.  1005 of 2048 slots of 152064 bf16 (0.31 GB read, 0.62 GB written) take 159 us =
 // 5.85 TB/s, 512 of 126464 fp32 with entropy 86 us = 6.0 TB/s.
 struct GradParams {
@@ -741,12 +741,15 @@ __global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(GradParams P
         }
     }
     const float2 st = P.stats[slot];
+    // log2 p = (x - m - log S) log2 e = y + rest + kLog2eShort y, with y in floats and `rest` what rounding nls left, so
+    // p = 2^y (c0 + c1 y).
     const float nls = -st.y * kLog2e;
-    float a = gl, b = 0.0f;
+    const float c0 = fmaf(kLn2, fmaf(-st.y, kLog2e, -nls), 1.0f), c1 = kLn2 * kLog2eShort;
+    float a = -gl, b = 0.0f;                   // the gradient is p (a + b log2 p)
     if (ENT) {
         const float gh = P.gh[slot];
-        a = fmaf(gh, P.entropy[slot], gl);
-        b = gh * kLn2;
+        a = -fmaf(gh, P.entropy[slot], gl);
+        b = -gh * kLn2;
     }
 #pragma unroll
     for (int i = 0; i < kGradVecs; ++i) {
@@ -757,9 +760,9 @@ __global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(GradParams P
         else load_vec_elems<BF16>(row, v, V, x);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float y = fmaf(x[e] - st.x, kLog2e, nls);
-            const float p = __builtin_amdgcn_exp2f(y);
-            g[e] = ENT ? -p * fmaf(fmaxf(y, kFarBelow), b, a) : -p * a;
+            const float y = fmaxf(fmaf(x[e] - st.x, kLog2e, nls), kFarBelow);
+            const float p = __builtin_amdgcn_exp2f(y) * fmaf(y, c1, c0);
+            g[e] = p * (ENT ? fmaf(y, b, a) : a);
         }
         if (tok >= 0 && tok / E == v) {
 #pragma unroll
