@@ -81,16 +81,22 @@ def _logits_shape(logits, rows, L, V, pos_stride, row_stride):
         rows, L, V = logits.shape
     if pos_stride is None and row_stride is None and logits.dim() != 3 and not logits.is_contiguous():
         raise ValueError(f"logits of shape {tuple(logits.shape)} with strides {logits.stride()} need pos_stride and row_stride")
+    cube = logits.dim() == 3
     if pos_stride is None:
-        pos_stride = logits.stride(1) if logits.dim() == 3 else V
+        pos_stride = logits.stride(1) if cube else V
+        if L == 1 and cube and not V <= pos_stride <= logits.stride(0):
+            pos_stride = V                      # a dimension of size 1 has a stride of any value
     if row_stride is None:
-        row_stride = logits.stride(0) if logits.dim() == 3 else L * pos_stride
+        row_stride = logits.stride(0) if cube else L * pos_stride
+        if rows == 1 and row_stride < L * pos_stride:
+            row_stride = L * pos_stride
     if rows > 0 and L > 0 and V > 0:
         reach = (rows - 1) * row_stride + (L - 1) * pos_stride + V
-        avail = logits.untyped_storage().nbytes() // logits.element_size() - logits.storage_offset()
-        if reach > avail:
-            raise ValueError(f"logits storage holds {avail} elements past its offset; rows={rows}, L={L}, V={V} "
-                             f"with strides ({row_stride}, {pos_stride}) reach {reach}")
+        if reach > logits.numel() or not logits.is_contiguous():
+            avail = logits.untyped_storage().nbytes() // logits.element_size() - logits.storage_offset()
+            if reach > avail:
+                raise ValueError(f"logits storage holds {avail} elements past its offset; rows={rows}, L={L}, V={V} "
+                                 f"with strides ({row_stride}, {pos_stride}) reach {reach}")
     return rows, L, V, pos_stride, row_stride
 
 
