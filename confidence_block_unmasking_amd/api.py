@@ -446,7 +446,14 @@ def dllm_logprobs_grad(logits, mask, tokens, stats, grad_logprob, grad_logits, s
         raise ValueError(f"grad_logits must be {logits.dtype}, got {grad_logits.dtype}")
     if grad_logits.dim() == 3 and tuple(grad_logits.shape) != (rows, L, V):
         raise ValueError(f"grad_logits of shape {tuple(grad_logits.shape)}, needs [{rows}, {L}, {V}]")
+    own_strides = grad_pos_stride is None and grad_row_stride is None and grad_logits.dim() == 3
     _, _, _, grad_pos_stride, grad_row_stride = _logits_shape(grad_logits, rows, L, V, grad_pos_stride, grad_row_stride)
+    if not own_strides and rows > 0:            # what is written has to lie in the tensor, not in its storage only
+        reach = (rows - 1) * grad_row_stride + (L - 1) * grad_pos_stride + V
+        own = 1 + sum((n - 1) * s for n, s in zip(grad_logits.shape, grad_logits.stride())) if grad_logits.numel() else 0
+        if reach > own:
+            raise ValueError(f"grad_logits of shape {tuple(grad_logits.shape)} spans {own} elements; rows={rows}, L={L}, V={V} "
+                             f"with strides ({grad_row_stride}, {grad_pos_stride}) reach {reach}")
     _need(mask, torch.uint8, "mask", rows * L, (L,))
     _need(stats, torch.float32, "stats", rows * L * 2, (L, 2))
     _need(status, torch.int32, "status", 1)

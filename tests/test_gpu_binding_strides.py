@@ -44,3 +44,46 @@ def test_padded_matrix_of_logits_needs_its_strides():
                            grad_pos_stride=pitch, grad_row_stride=L * pitch, **size)
     assert torch.equal(grad[:rows * L, :V], other) and (grad[:, V:] == 7.0).all() and (grad[rows * L:] == 7.0).all()
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("make,strides", [
+    (lambda b: b[:100], {}), (lambda b: b[:239], {}), (lambda b: b[:240], dict(grad_pos_stride=41, grad_row_stride=123)),
+    (lambda b: b[:240].view(6, 40)[:5], {}), (lambda b: b[:240].view(2, 3, 40), dict(grad_pos_stride=48, grad_row_stride=144)),
+    (lambda b: b[:0], {})])
+def test_gradient_stays_in_its_tensor(make, strides):
+    """A view too small for the gradient, in a storage that would hold it: what lies behind the view is
+    not the call's."""
+    from confidence_block_unmasking_amd import api
+    rows, L, V = 2, 3, 40
+    f = dict(dtype=torch.float32, device="cuda")
+    buf = torch.full((4096,), 7.0, **f)
+    mask, tok = torch.ones((rows, L), dtype=torch.uint8, device="cuda"), torch.zeros((rows, L), dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        api.dllm_logprobs_grad(torch.randn((rows, L, V), **f), mask, tok, torch.zeros((rows, L, 2), **f), torch.ones((rows, L), **f),
+                               make(buf), st, rows=rows, L=L, V=V, **strides)
+    torch.cuda.synchronize()
+    assert (buf == 7.0).all()
+
+
+def test_gradient_into_views_that_hold_it():
+    from confidence_block_unmasking_amd import api
+    rows, L, V = 2, 3, 40
+    f = dict(dtype=torch.float32, device="cuda")
+    lg = torch.randn((rows, L, V), **f)
+    mask, tok = torch.ones((rows, L), dtype=torch.uint8, device="cuda"), torch.zeros((rows, L), dtype=torch.int32, device="cuda")
+    sta, one, st = torch.zeros((rows, L, 2), **f), torch.ones((rows, L), **f), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ref = torch.empty((rows, L, V), **f)
+    api.dllm_logprobs_grad(lg, mask, tok, sta, one, ref, st)
+    for shape, strides, pitch in (((240,), {}, 40), ((6, 40), {}, 40), ((300,), {}, 40),
+                                  ((286,), dict(grad_pos_stride=48, grad_row_stride=150), 48)):
+        buf = torch.full((512,), 7.0, **f)
+        n = 1
+        for d in shape:
+            n *= d
+        api.dllm_logprobs_grad(lg, mask, tok, sta, one, buf[:n].view(shape), st, rows=rows, L=L, V=V, **strides)
+        at = [(r * strides.get("grad_row_stride", L * pitch) + j * pitch, r, j) for r in range(rows) for j in range(L)]
+        for a, r, j in at:
+            assert torch.equal(buf[a:a + V], ref[r, j])
+        assert (buf[at[-1][0] + V:] == 7.0).all()
+    assert int(st.item()) == 0
