@@ -269,8 +269,8 @@ __device__ __forceinline__ float4 chunk_record(float (&x)[kVPL][E], float &lm, f
 }
 
 // Kernel 1: one record per chunk of every selected slot, and its lanes' maxima.  Bound by HBM: 1005 slots of
-// 152064 bf16 (305.6 MB) take 51.6 us = 5.9 TB/s, 16384 (4.98 GB) 779 us = 6.4 TB/s; a plain read of as much
-// reaches 6.4 and 7.0.  Few slots are bound by the prologue and one chunk's latency (192: 15.7 us, one: 5.4).
+// 152064 bf16 (305.6 MB) take 52.5 us = 5.8 TB/s, 16384 (4.98 GB) 795 us = 6.3 TB/s; a plain read of as much
+// reaches 6.4 and 7.0.  Few slots are bound by the prologue and the latency of a few chunks (192: 15.9 us, one: 5.3).
 template <bool BF16, bool ENT, bool TOP>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) void logprob_chunks_kernel(LogprobParams P) {
     extern __shared__ int s_id[];              // [win] selected slots of this workgroup's window
@@ -346,7 +346,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
 }
 
 // Kernel 2, without alternatives: one wave per slot.  Bound by latency (token, then its logit, beside the
-// records): 10.2 us for 16384 slots.
+// records) and, with many slots, by log(1 + r): 12.8 us for 16384 (10.2 with log S).
 constexpr int kJoinWaves = 4;
 
 struct Softmax {
@@ -594,7 +594,7 @@ __device__ __forceinline__ void top_of_slot(const LogprobParams &P, TopShared<WA
 }
 
 // Kernel 2, with alternatives: one workgroup per slot.  Bound by latency (mask, maxima, shares, each a round trip
-// behind the other, and three barriers): 6.3 us for one slot, 15.2 us for 1005 with k = 20, where 4 waves per slot
+// behind the other, and three barriers): 6.5 us for one slot, 15.8 us for 1005 with k = 20, where 4 waves per slot
 // are better than 2 (19) and 8 (17).
 template <bool BF16>
 __global__ __launch_bounds__(64 * kJoinWaves) void logprob_top_kernel(LogprobParams P) {
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprob_top_kernel(LogprobPar
 // ---- one kernel -----------------------------------------------------------------------------------
 // For few short rows: a workgroup per slot.  Its waves take the slot's chunks in turn, keep records and lane
 // maxima in LDS, and finish the slot there (the same arithmetic in the same order: the same bits), which
-// saves the second launch and the mask scan.  Bound by latency: 231 slots of 20011 fp32 with k = 20 take 11 us.
+// saves the second launch and the mask scan.  Bound by latency: 231 slots of 20011 fp32 with k = 20 take 11.3 us.
 constexpr int kShortRow = 16;                  // chunks of a row at most
 
 template <bool BF16, bool ENT, bool TOP>
@@ -678,7 +678,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4))) v
 // by HBM; per element an unpack, a subtraction, an FMA, a max, v_exp, an FMA and two multiplications (with entropy
 // also an FMA) and half a pack.  A thread reads its vectors before it writes them, so the gradient
 // may replace the logits in place.  1005 of 2048 slots of 152064 bf16 (0.31 GB read, 0.62 GB written) take 159 us =
-// 5.85 TB/s, 512 of 126464 fp32 with entropy 86 us = 6.0 TB/s.
+// 5.85 TB/s, 512 of 126464 fp32 with entropy 88 us = 5.9 TB/s.
 struct GradParams {
     const char *logits;
     int64_t pos_stride_b, row_stride_b;
