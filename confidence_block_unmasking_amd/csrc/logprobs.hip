@@ -760,9 +760,9 @@ __global__ __launch_bounds__(kGradThreads) void logprob_grad_kernel(GradParams P
         else load_vec_elems<BF16>(row, v, V, x);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float y = fmaxf(fmaf(x[e] - st.x, kLog2e, nls), kFarBelow);
-            const float p = __builtin_amdgcn_exp2f(y) * fmaf(y, c1, c0);
-            g[e] = p * (ENT ? fmaf(y, b, a) : a);
+            const float y = fmaf(x[e] - st.x, kLog2e, nls), yf = fmaxf(y, kFarBelow);   // finite beside a power of 0
+            const float p = __builtin_amdgcn_exp2f(y) * fmaf(yf, c1, c0);
+            g[e] = p * (ENT ? fmaf(yf, b, a) : a);
         }
         if (tok >= 0 && tok / E == v) {
 #pragma unroll

@@ -116,3 +116,28 @@ def test_gradient_of_slots_without_a_distribution_is_nan(dtype):
         nan = out[0].isnan().cpu().numpy()
         assert nan[bad].all() and not nan[~bad].any()
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_gradient_of_a_nan_logit_is_nan_whatever_the_statistics(dtype, entropy):
+    """Statistics of other logits (a caller's mistake) do not hide a NaN: its column reads NaN, the others
+    the formula's values."""
+    from confidence_block_unmasking_amd import api
+    V, f = 1030, dict(dtype=torch.float32, device="cuda")
+    t = torch.randn((1, 2, V), generator=torch.Generator().manual_seed(5)).to(DT[dtype])
+    g, _ = run(t.view(-1).cuda(), 1, 2, V, V, 0, np.ones((1, 2), bool), np.zeros((1, 2)), 0)
+    one, st = torch.ones((1, 2), **f), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ent = dict(entropy=torch.from_numpy(g["entropy"]).cuda(), grad_entropy=one) if entropy else {}
+    out = []
+    for plant in (False, True):
+        x = t.clone()
+        if plant:
+            x[0, 1, [3, V - 1]] = float("nan")
+        out.append(torch.zeros((1, 2, V), dtype=DT[dtype], device="cuda"))
+        api.dllm_logprobs_grad(x.cuda(), torch.ones((1, 2), dtype=torch.uint8, device="cuda"),
+                               torch.zeros((1, 2), dtype=torch.int32, device="cuda"), torch.from_numpy(g["stats"]).cuda(), one, out[-1], st,
+                               **ent)
+    nan = torch.zeros((1, 2, V), dtype=torch.bool, device="cuda")
+    nan[0, 1, [3, V - 1]] = True
+    assert torch.equal(out[1].isnan(), nan) and torch.equal(out[1][~nan], out[0][~nan])
