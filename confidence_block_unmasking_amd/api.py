@@ -494,18 +494,18 @@ def _matrix(t, name):
 
 def _ids_arg(ids, valid, status):
     _need(ids, torch.int32, "ids")
+    n = ids.numel()
     if valid is not None:
-        _need(valid, torch.uint8, "valid", ids.numel())
+        _need(valid, torch.uint8, "valid", n, () if valid.numel() == n else ids.shape[1:])
     _need(status, torch.int32, "status", 1)
-    return ids.numel()
+    return n
 
 
-def _same_box(t, name, n_rows, ids, n):
-    """Refuse a box [..., W', D] whose rows of W' are not the ids' rows: its first n of n_rows rows of D are used as
-    one run.  (A matrix [n_rows, D], or as many rows as ids, leaves no doubt; flat ids may be any whole rows.)"""
-    if t.dim() > 2 and n_rows != n:
-        if (t.shape[1:-1] != ids.shape[1:]) if ids.dim() > 1 else (n % max(t.shape[-2], 1) != 0):
-            raise ValueError(f"{name} of shape {tuple(t.shape)} for ids of shape {tuple(ids.shape)}")
+def _same_box(t, name, ids, n):
+    """Refuse a box [..., W', D] of more rows of D than the n ids whose rows of W' are not the ids' rows: its first n
+    are used as one run.  (A matrix [n_rows, D] leaves no doubt; flat ids may be any whole rows.)"""
+    if t.dim() > 2 and ((t.shape[1:-1] != ids.shape[1:]) if ids.dim() > 1 else (n % max(t.shape[-2], 1) != 0)):
+        raise ValueError(f"{name} of shape {tuple(t.shape)} for ids of shape {tuple(ids.shape)}")
 
 
 def dllm_embed(table, ids, out, status, valid=None, scale=1.0, stream=None):
@@ -518,7 +518,8 @@ def dllm_embed(table, ids, out, status, valid=None, scale=1.0, stream=None):
     n_out, D_out, os_ = _matrix(out, "out")
     if D_out != D or n_out < n:
         raise ValueError(f"out holds {n_out} rows of {D_out}, needs {n} of {D}")
-    _same_box(out, "out", n_out, ids, n)
+    if n_out != n:
+        _same_box(out, "out", ids, n)
     if (n | n_vocab | D) >> 31:
         _fits("dllm_embed", n, n_vocab, D)
     _call(_lib.lib().dllm_embed, "dllm_embed", stream, (table, ids, valid, out, status),
@@ -546,7 +547,8 @@ def dllm_embed_grad(grad_out, ids, grad_table, workspace, status, valid=None, sc
     n_grad, D_grad, gs = _matrix(grad_out, "grad_out")
     if D_grad != D or n_grad < n:
         raise ValueError(f"grad_out holds {n_grad} rows of {D_grad}, needs {n} of {D}")
-    _same_box(grad_out, "grad_out", n_grad, ids, n)
+    if n_grad != n:
+        _same_box(grad_out, "grad_out", ids, n)
     _need(workspace, torch.uint8, "workspace")
     if (n | n_vocab | D) >> 31:
         _fits("dllm_embed_grad", n, n_vocab, D)

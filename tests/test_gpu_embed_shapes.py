@@ -66,3 +66,26 @@ def test_session_embeds_into_a_buffer_of_its_width_only():
     with pytest.raises(ValueError):
         s.embed(table, out=torch.empty((s.rows, s.W + 3, 24), device="cuda"))
     s.check_status("dllm_embed")
+
+
+def test_valid_of_a_wider_box_is_refused():
+    from confidence_block_unmasking_amd import api
+    a = _inputs()
+    out, grad = torch.full((3, 5, 8), 7.0, device="cuda"), torch.full_like(a["table"], 7.0)
+    ws = api.new_embed_grad_workspace(15, 11, 8)
+    wide = torch.ones((3, 7), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        api.dllm_embed(a["table"], a["ids"], out, a["status"], valid=wide)
+    with pytest.raises(ValueError):
+        api.dllm_embed_grad(out, a["ids"], grad, ws, a["status"], valid=wide)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and (grad == 7.0).all()
+    for shape in ((3, 5), (4, 5), (15,), (19,), (2, 3, 5)):
+        out.fill_(7.0)
+        valid = torch.ones(shape, dtype=torch.uint8, device="cuda")
+        valid.view(-1)[3] = 0
+        api.dllm_embed(a["table"], a["ids"], out, a["status"], valid=valid)
+        ref = a["table"][a["ids"].long()]
+        ref.view(-1, 8)[3] = 0.0
+        assert torch.equal(out, ref)
+    assert int(a["status"].item()) == 0
